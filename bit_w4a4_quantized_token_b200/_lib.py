@@ -26,6 +26,10 @@ SVDQ_INT4 = 1
 PRECISIONS = {"nvfp4": SVDQ_NVFP4, "int4": SVDQ_INT4}
 GROUP_SIZES = {"nvfp4": 16, "int4": 64}
 
+SVDQ_BF16 = 0
+SVDQ_F16 = 1
+SVDQ_F32 = 2
+
 # Every entry point declared in include/svdq.h.
 EXPORTS = (
     "svdq_status_string", "svdq_abi_version", "svdq_last_error", "svdq_buffer_sizes", "svdq_pack_weight",
@@ -34,6 +38,7 @@ EXPORTS = (
     "svdq_gemm_w4a4_qkv_norm_rope", "svdq_qkv_norm_rope", "svdq_gelu_mlp_workspace_bytes",
     "svdq_gemm_w4a4_gelu_quant", "svdq_gemm_w4a4_gelu", "svdq_gelu", "svdq_gemm_w4a16", "svdq_svd_split_workspace_bytes",
     "svdq_svd_split",
+    "svdq_pack_weight_w8a8", "svdq_quantize_act_w8a8", "svdq_rms_norm_quantize_w8a8", "svdq_gemm_w8a8",
     "svdq_device_status",
     "svdq_debug_set_wait_limit_ns", "svdq_debug_timeout_probe", "svdq_debug_override_capability",
     "svdq_debug_force_gemm_tiles", "svdq_debug_force_quant_plan",
@@ -97,6 +102,14 @@ def _load():
     lib.svdq_gelu.restype = I
     lib.svdq_gemm_w4a16.argtypes = [P, I64, P, P, I64, I64, P, P, P]
     lib.svdq_gemm_w4a16.restype = I
+    lib.svdq_pack_weight_w8a8.argtypes = [I, P, I64, I64, P, P, P, P, P]
+    lib.svdq_pack_weight_w8a8.restype = I
+    lib.svdq_quantize_act_w8a8.argtypes = [I, P, I64, I64, I64, P, P, P, P]
+    lib.svdq_quantize_act_w8a8.restype = I
+    lib.svdq_rms_norm_quantize_w8a8.argtypes = [I, P, I64, P, I64, I64, I64, P, F, P, P, P, P, P, P]
+    lib.svdq_rms_norm_quantize_w8a8.restype = I
+    lib.svdq_gemm_w8a8.argtypes = [P, P, I64, P, P, I64, I64, P, I, P, P]
+    lib.svdq_gemm_w8a8.restype = I
     lib.svdq_svd_split_workspace_bytes.argtypes = [I64, I64, I, I, ctypes.POINTER(ctypes.c_size_t)]
     lib.svdq_svd_split_workspace_bytes.restype = I
     lib.svdq_svd_split.argtypes = [P, P, I64, I64, I, P, I, I, P, P, P, P, P, ctypes.c_size_t, P]
@@ -268,6 +281,29 @@ def svdq_gemm_w4a16(x, M, w_codes, w_scales, N, K, bias, y, stream=None) -> None
                                _stream(stream)), "svdq_gemm_w4a16")
 
 
+def svdq_pack_weight_w8a8(w_type, W, N, K, lam, w_codes, w_scales, inv_lambda, stream=None) -> None:
+    _check(lib.svdq_pack_weight_w8a8(int(w_type), _ptr(W), int(N), int(K), _ptr(lam), _ptr(w_codes), _ptr(w_scales),
+                                     _ptr(inv_lambda), _stream(stream)), "svdq_pack_weight_w8a8")
+
+
+def svdq_quantize_act_w8a8(x_type, x, ldx, M, K, inv_lambda, x_codes, x_scales, stream=None) -> None:
+    _check(lib.svdq_quantize_act_w8a8(int(x_type), _ptr(x), int(ldx), int(M), int(K), _ptr(inv_lambda),
+                                      _ptr(x_codes), _ptr(x_scales), _stream(stream)), "svdq_quantize_act_w8a8")
+
+
+def svdq_rms_norm_quantize_w8a8(x_type, x, ldx, residual, ldr, M, K, norm_weight, eps, inv_lambda, h_out, normed,
+                                x_codes, x_scales, stream=None) -> None:
+    _check(lib.svdq_rms_norm_quantize_w8a8(int(x_type), _ptr(x), int(ldx), _ptr(residual), int(ldr), int(M), int(K),
+                                           _ptr(norm_weight), float(eps), _ptr(inv_lambda), _ptr(h_out),
+                                           _ptr(normed), _ptr(x_codes), _ptr(x_scales), _stream(stream)),
+           "svdq_rms_norm_quantize_w8a8")
+
+
+def svdq_gemm_w8a8(x_codes, x_scales, M, w_codes, w_scales, N, K, bias, y_type, y, stream=None) -> None:
+    _check(lib.svdq_gemm_w8a8(_ptr(x_codes), _ptr(x_scales), int(M), _ptr(w_codes), _ptr(w_scales), int(N), int(K),
+                              _ptr(bias), int(y_type), _ptr(y), _stream(stream)), "svdq_gemm_w8a8")
+
+
 def svdq_svd_split_workspace_bytes(N: int, K: int, rank: int, oversample: int) -> int:
     out = ctypes.c_size_t(0)
     _check(lib.svdq_svd_split_workspace_bytes(int(N), int(K), int(rank), int(oversample), ctypes.byref(out)),
@@ -304,7 +340,7 @@ def svdq_debug_override_capability(major: int, minor: int = 0) -> None:
 
 
 def svdq_debug_force_gemm_tiles(mode: int) -> None:
-    """nvfp4 GEMM kernel: 0 = automatic, 1 = single-CTA 128x256 tiles, 2 = CTA-pair tiles."""
+    """nvfp4 and W8A8 GEMM kernels: 0 = automatic, 1 = single-CTA tiles, 2 = CTA-pair tiles."""
     _check(lib.svdq_debug_force_gemm_tiles(int(mode)), "svdq_debug_force_gemm_tiles")
 
 

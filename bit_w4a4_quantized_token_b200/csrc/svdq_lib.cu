@@ -21,6 +21,8 @@
 #include "qkv_norm_rope.cuh"
 #include "svd_split.cuh"
 #include "gemm_dq16.cuh"
+#include "quantize_w8a8.cuh"
+#include "gemm_w8a8.cuh"
 
 namespace svdq {
 namespace {
@@ -72,6 +74,8 @@ bool g_device_ready[kMaxDevices];
 // Budget of dynamic shared memory for the activation quantizer (the opt-in
 // maximum is 227 KB per block including static shared memory).
 constexpr int kQuantSmemBudget = 226 * 1024;
+// The same for the narrow W8A8 GEMM when one block runs per SM.
+constexpr int kNarrowSmemBudget = 224 * 1024;
 
 thread_local char g_last_error[256] = "";
 
@@ -132,7 +136,21 @@ svdq_status check_device() {
             cudaFuncSetAttribute(gemm_nvfp4_pair_kernel<kEpiGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)gp::SMEM_BYTES_GELU) != cudaSuccess ||
             cudaFuncSetAttribute(gemm_nvfp4_pair_kernel<kEpiGeluStore>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)gp::SMEM_BYTES_GELU) != cudaSuccess)
+                                 (int)gp::SMEM_BYTES_GELU) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_pair_kernel<kBf16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)w8p::SMEM_BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_pair_kernel<kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)w8p::SMEM_BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_pair_kernel<kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)w8p::SMEM_BYTES) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kNarrowSmemBudget) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kNarrowSmemBudget) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kNarrowSmemBudget) != cudaSuccess ||
+            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kNarrowSmemBudget) != cudaSuccess)
             return cuda_fail("setting kernel shared-memory limits");
         g_device_ready[dev] = true;
     }
@@ -735,6 +753,174 @@ svdq_status dq16_gemm(bool int4_a, const void* a_codes, const void* a_scales, in
     return launch_status("gemm_dq16_kernel launch");
 }
 
+// --------------------------------------------------------------- W8A8 paths
+svdq_status check_dtype(svdq_dtype t) {
+    return (t == SVDQ_BF16 || t == SVDQ_F16 || t == SVDQ_F32) ? SVDQ_OK : SVDQ_ERR_INVALID_ARG;
+}
+int64_t dtype_bytes(svdq_dtype t) { return t == SVDQ_F32 ? 4 : 2; }
+
+svdq_status check_dims_w8a8(int64_t rows, int64_t K) {
+    if (rows < 1 || rows >= (int64_t(1) << 31)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (K < 16 || K >= (int64_t(1) << 17) || K % 16 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    return SVDQ_OK;
+}
+
+// A row stride in elements: at least K, and a multiple of 16 bytes.
+svdq_status check_stride(int64_t ld, int64_t K, svdq_dtype t) {
+    if (ld < K || ld >= (int64_t(1) << 31) || ld * dtype_bytes(t) % 16 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    return SVDQ_OK;
+}
+
+// Whether the byte ranges [p, p + np) and [q, q + nq) share memory.
+bool overlaps(const void* p, int64_t np, const void* q, int64_t nq) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return p != nullptr && q != nullptr && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
+}
+
+// Blocks of `threads` threads that one SM holds, looked up once per device.
+template <typename Kernel>
+int blocks_per_sm(Kernel kernel, int threads, std::atomic<int>* cache) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return 1;
+    }
+    std::atomic<int>& slot = cache[dev * 33 + threads / 32];
+    int n = slot.load();
+    if (n == 0) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+        slot.store(n);
+    }
+    return n;
+}
+
+template <typename Kernel>
+svdq_status launch_rows(Kernel kernel, int threads, std::atomic<int>* cache, const QuantRowsArgs& a, cudaStream_t st) {
+    const int64_t grid = std::min<int64_t>(a.M, (int64_t)num_sms() * blocks_per_sm(kernel, threads, cache));
+    if (launch_ex(kernel, dim3((unsigned)grid), dim3((unsigned)threads), 0, st, 1u, a) != cudaSuccess)
+        return cuda_fail("quantize_rows_w8_kernel launch");
+    return launch_status("quantize_rows_w8_kernel launch");
+}
+
+template <int T, bool NORM, int V>
+svdq_status quantize_rows_held(const QuantRowsArgs& a, cudaStream_t st) {
+    static std::atomic<int> cache[kMaxDevices * 33];
+    const int threads = (int)round_up((a.K / 8 + V - 1) / V, 32);
+    return launch_rows(quantize_rows_w8_kernel<T, NORM, V>, threads, cache, a, st);
+}
+
+template <int T, bool NORM>
+svdq_status quantize_rows_typed(const QuantRowsArgs& a, cudaStream_t st) {
+    const int nvec = a.K / 8;
+    constexpr int kMaxV = T == kF32 && NORM ? 2 : 4;   // what fits in registers without spilling
+    if (nvec <= 256) return quantize_rows_held<T, NORM, 1>(a, st);
+    if (nvec <= 1024) return quantize_rows_held<T, NORM, 2>(a, st);
+    if (nvec <= kMaxV * q8::kMaxThreads) return quantize_rows_held<T, NORM, kMaxV>(a, st);
+    static std::atomic<int> cache[kMaxDevices * 33];
+    return launch_rows(quantize_rows_w8_wide_kernel<T, NORM>, q8::kTwoPassThreads, cache, a, st);
+}
+
+template <bool NORM>
+svdq_status quantize_rows_w8(svdq_dtype t, const QuantRowsArgs& a, cudaStream_t st) {
+    if (t == SVDQ_F32) return quantize_rows_typed<kF32, NORM>(a, st);
+    if (t == SVDQ_F16) return quantize_rows_typed<kF16, NORM>(a, st);
+    return quantize_rows_typed<kBf16, NORM>(a, st);
+}
+
+// How svdq_gemm_w8a8 runs a shape.
+struct W8Plan {
+    bool pair;
+    int nt, split, stages;   // narrow kernel: tokens of a tile, CTAs sharing its K range, ring depth
+};
+W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
+    const int64_t chunks = (K + w8n::BK - 1) / w8n::BK;
+    const int64_t pair_tiles = ((M + w8p::BM - 1) / w8p::BM) * ((N + w8p::BN - 1) / w8p::BN);
+    const int mode = g_gemm_tiles_mode.load();
+    W8Plan p = {};
+    p.pair = mode == 2 || (mode == 0 && M > 128 && pair_tiles >= 40);
+    if (p.pair) return p;
+    p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    const int64_t tiles = ((M + p.nt - 1) / p.nt) * ((N + w8n::BN - 1) / w8n::BN);
+    const int sms = num_sms();
+    p.split = 1;
+    while (p.split < w8n::kMaxSplit && tiles * p.split * 2 <= 2 * sms && chunks / (2 * p.split) >= 4) p.split *= 2;
+    const bool two = tiles * p.split > sms;   // two blocks per SM
+    const int budget = (two ? kNarrowSmemBudget / 2 : kNarrowSmemBudget) - w8n::fixed_bytes(p.nt);
+    const int64_t most = (chunks + p.split - 1) / p.split;
+    p.stages = (int)std::min<int64_t>({(int64_t)w8n::kMaxStages, (int64_t)(budget / w8n::stage_bytes(p.nt)), most});
+    // the partial sums need the room of the ring
+    const int need = (w8n::partial_bytes(p.nt) + w8n::stage_bytes(p.nt) - 1) / w8n::stage_bytes(p.nt);
+    if (p.split > 1) p.stages = std::max(p.stages, need);
+    return p;
+}
+
+template <int NT>
+svdq_status gemm_w8a8_narrow(const W8Plan& p, const CUtensorMap& tm_x, const CUtensorMap& tm_w, GemmW8Args a,
+                             cudaStream_t st) {
+    a.stages = p.stages;
+    const size_t smem = (size_t)w8n::fixed_bytes(NT) + (size_t)p.stages * w8n::stage_bytes(NT);
+    const dim3 grid((unsigned)p.split, (unsigned)a.n_tiles, (unsigned)a.m_tiles);
+    if (launch_ex(gemm_w8a8_narrow_kernel<NT>, grid, dim3(w8n::kThreads), smem, st, (unsigned)p.split, tm_x, tm_w,
+                  a) != cudaSuccess)
+        return cuda_fail("gemm_w8a8_narrow_kernel launch");
+    return launch_status("gemm_w8a8_narrow_kernel launch");
+}
+
+svdq_status gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, const void* w_codes,
+                      const float* w_scales, int64_t N, int64_t K, const void* bias, svdq_dtype out, void* y,
+                      cudaStream_t st) {
+    const W8Plan p = w8_plan(M, N, K);
+    GemmW8Args a = {};
+    a.x_scales = x_scales;
+    a.w_scales = w_scales;
+    a.bias = bias;
+    a.y = y;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.chunks = (int)((K + 127) / 128);
+    a.last_steps = (int)((K - 128 * (int64_t)(a.chunks - 1) + 31) / 32);
+    a.out = out;
+    const int64_t tm = p.pair ? w8p::BM : p.nt, tn = p.pair ? w8p::BN : w8n::BN;
+    const int64_t mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
+    if (p.pair ? mt * nt > (int64_t(1) << 30) : (mt > 65535 || nt > 65535)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    a.m_tiles = (int)mt;
+    a.n_tiles = (int)nt;
+    CUtensorMap tm_x, tm_w;
+    if (!make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_codes, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
+                  p.pair ? 128 : (uint32_t)p.nt) ||
+        !make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128))
+        return SVDQ_ERR_CUDA;
+    if (!p.pair) {
+        if (p.nt == 16) return gemm_w8a8_narrow<16>(p, tm_x, tm_w, a, st);
+        if (p.nt == 32) return gemm_w8a8_narrow<32>(p, tm_x, tm_w, a, st);
+        if (p.nt == 64) return gemm_w8a8_narrow<64>(p, tm_x, tm_w, a, st);
+        return gemm_w8a8_narrow<128>(p, tm_x, tm_w, a, st);
+    }
+    // y leaves through TMA stores of boxes of 32 rows x 64 bytes
+    CUtensorMap tm_y;
+    const CUtensorMapDataType yt = out == SVDQ_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : out == SVDQ_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int64_t yb = dtype_bytes(out);
+    if (!make_map(&tm_y, yt, y, (uint64_t)N, (uint64_t)M, (uint64_t)(N * yb), (uint32_t)(64 / yb), 32,
+                  CU_TENSOR_MAP_SWIZZLE_64B))
+        return SVDQ_ERR_CUDA;
+    const unsigned clusters = (unsigned)std::min<int64_t>(mt * nt, pair_clusters());
+    const dim3 grid(2 * clusters), block(w8p::kThreads);
+    cudaError_t e;
+    if (out == SVDQ_F32)
+        e = launch_ex(gemm_w8a8_pair_kernel<kF32>, grid, block, w8p::SMEM_BYTES, st, 2u, tm_x, tm_w, tm_y, a);
+    else if (out == SVDQ_F16)
+        e = launch_ex(gemm_w8a8_pair_kernel<kF16>, grid, block, w8p::SMEM_BYTES, st, 2u, tm_x, tm_w, tm_y, a);
+    else
+        e = launch_ex(gemm_w8a8_pair_kernel<kBf16>, grid, block, w8p::SMEM_BYTES, st, 2u, tm_x, tm_w, tm_y, a);
+    if (e != cudaSuccess) return cuda_fail("gemm_w8a8_pair_kernel launch");
+    return launch_status("gemm_w8a8_pair_kernel launch");
+}
+
 // Kernel that waits on a barrier nobody completes: exercises the bounded wait.
 __global__ void timeout_probe_kernel() {
     __shared__ uint64_t bar;
@@ -1198,6 +1384,119 @@ svdq_status svdq_gemm_w4a16(const void* x, int64_t M, const void* w_codes, const
     SVDQ_TRY(check_opt_ptr(bias));
     SVDQ_TRY(check_device());
     return dq16_gemm(false, x, nullptr, M, w_codes, w_scales, N, K, nullptr, nullptr, 0, bias, y,
+                     reinterpret_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_pack_weight_w8a8(svdq_dtype w_type, const void* W, int64_t N, int64_t K, const float* lambda,
+                                  void* w_codes, float* w_scales, float* inv_lambda, svdq_stream_t stream) {
+    SVDQ_TRY(check_dtype(w_type));
+    SVDQ_TRY(check_dims_w8a8(N, K));
+    SVDQ_TRY(check_ptr(W));
+    SVDQ_TRY(check_ptr(w_codes));
+    SVDQ_TRY(check_ptr(w_scales));
+    SVDQ_TRY(check_opt_ptr(lambda));
+    SVDQ_TRY(lambda ? check_ptr(inv_lambda) : check_opt_ptr(inv_lambda));
+    SVDQ_TRY(check_device());
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (lambda) SVDQ_TRY(fold_lowrank(lambda, nullptr, nullptr, N, K, 0, inv_lambda, nullptr, nullptr, st));
+    QuantRowsArgs a = {};
+    a.x = W;
+    a.gain = lambda;
+    a.codes = reinterpret_cast<uint8_t*>(w_codes);
+    a.scales = w_scales;
+    a.ldx = K;
+    a.M = (int)N;
+    a.K = (int)K;
+    return quantize_rows_w8<false>(w_type, a, st);
+}
+
+svdq_status svdq_quantize_act_w8a8(svdq_dtype x_type, const void* x, int64_t ldx, int64_t M, int64_t K,
+                                   const float* inv_lambda, void* x_codes, float* x_scales, svdq_stream_t stream) {
+    SVDQ_TRY(check_dtype(x_type));
+    SVDQ_TRY(check_dims_w8a8(M, K));
+    SVDQ_TRY(check_stride(ldx, K, x_type));
+    SVDQ_TRY(check_ptr(x));
+    SVDQ_TRY(check_opt_ptr(inv_lambda));
+    SVDQ_TRY(check_ptr(x_codes));
+    SVDQ_TRY(check_ptr(x_scales));
+    if (overlaps(x, ((M - 1) * ldx + K) * dtype_bytes(x_type), x_codes, M * K)) return SVDQ_ERR_INVALID_ARG;
+    SVDQ_TRY(check_device());
+    QuantRowsArgs a = {};
+    a.x = x;
+    a.gain = inv_lambda;
+    a.codes = reinterpret_cast<uint8_t*>(x_codes);
+    a.scales = x_scales;
+    a.ldx = ldx;
+    a.M = (int)M;
+    a.K = (int)K;
+    return quantize_rows_w8<false>(x_type, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_rms_norm_quantize_w8a8(svdq_dtype x_type, const void* x, int64_t ldx, const void* residual,
+                                        int64_t ldr, int64_t M, int64_t K, const void* norm_weight, float eps,
+                                        const float* inv_lambda, void* h_out, void* normed, void* x_codes,
+                                        float* x_scales, svdq_stream_t stream) {
+    SVDQ_TRY(check_dtype(x_type));
+    SVDQ_TRY(check_dims_w8a8(M, K));
+    SVDQ_TRY(check_stride(ldx, K, x_type));
+    if (residual) SVDQ_TRY(check_stride(ldr, K, x_type));
+    if (!(eps > 0.0f) || !(eps < 1.0f)) return SVDQ_ERR_INVALID_ARG;
+    SVDQ_TRY(check_ptr(x));
+    SVDQ_TRY(check_opt_ptr(residual));
+    SVDQ_TRY(check_opt_ptr(norm_weight));
+    SVDQ_TRY(check_opt_ptr(inv_lambda));
+    SVDQ_TRY(check_opt_ptr(h_out));
+    SVDQ_TRY(check_opt_ptr(normed));
+    SVDQ_TRY(check_opt_ptr(x_codes));
+    SVDQ_TRY(check_opt_ptr(x_scales));
+    if ((x_codes == nullptr) != (x_scales == nullptr)) return SVDQ_ERR_INVALID_ARG;
+    if (x_codes == nullptr && normed == nullptr) return SVDQ_ERR_INVALID_ARG;
+    // an output may share memory with an input only as h_out does in place:
+    // the same rows at the same addresses
+    const int64_t b = dtype_bytes(x_type), out_bytes = M * K * b;
+    const int64_t x_bytes = ((M - 1) * ldx + K) * b, r_bytes = ((M - 1) * ldr + K) * b;
+    const bool h_on_x = h_out == x && (ldx == K || M == 1);
+    const bool h_on_r = h_out == residual && (ldr == K || M == 1);
+    if ((!h_on_x && overlaps(h_out, out_bytes, x, x_bytes)) ||
+        (!h_on_r && residual && overlaps(h_out, out_bytes, residual, r_bytes)) ||
+        overlaps(normed, out_bytes, x, x_bytes) || (residual && overlaps(normed, out_bytes, residual, r_bytes)) ||
+        overlaps(x_codes, M * K, x, x_bytes) || (residual && overlaps(x_codes, M * K, residual, r_bytes)) ||
+        overlaps(normed, out_bytes, h_out, out_bytes) || overlaps(x_codes, M * K, h_out, out_bytes) ||
+        overlaps(x_codes, M * K, normed, out_bytes))
+        return SVDQ_ERR_INVALID_ARG;
+    SVDQ_TRY(check_device());
+    QuantRowsArgs a = {};
+    a.x = x;
+    a.residual = residual;
+    a.norm_weight = norm_weight;
+    a.gain = inv_lambda;
+    a.h_out = h_out;
+    a.normed = normed;
+    a.codes = reinterpret_cast<uint8_t*>(x_codes);
+    a.scales = x_scales;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.M = (int)M;
+    a.K = (int)K;
+    a.eps = eps;
+    return quantize_rows_w8<true>(x_type, a, reinterpret_cast<cudaStream_t>(stream));
+}
+
+svdq_status svdq_gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, const void* w_codes,
+                           const float* w_scales, int64_t N, int64_t K, const void* bias, svdq_dtype y_type, void* y,
+                           svdq_stream_t stream) {
+    SVDQ_TRY(check_dtype(y_type));
+    SVDQ_TRY(check_dims_w8a8(M, K));
+    SVDQ_TRY(check_dims_w8a8(N, K));
+    if (N % 8 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    SVDQ_TRY(check_ptr(x_codes));
+    SVDQ_TRY(check_ptr(x_scales));
+    SVDQ_TRY(check_ptr(w_codes));
+    SVDQ_TRY(check_ptr(w_scales));
+    SVDQ_TRY(check_opt_ptr(bias));
+    SVDQ_TRY(check_ptr(y));
+    SVDQ_TRY(check_device());
+    return gemm_w8a8(x_codes, x_scales, M, w_codes, w_scales, N, K, bias, y_type, y,
                      reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -4,6 +4,13 @@ come from PyTorch; every step of the layer runs in the CUDA library.
 
     packed = pack_weight(R, lam, L_down, L_up, precision="nvfp4")   # once per layer
     y = svdq_linear(x, packed)                                      # quantize_act + gemm_w4a4
+
+The 8-bit integer (W8A8) layer, for the layers that 4 bits cost too much:
+
+    packed = pack_weight_w8a8(W, lam, bias)                         # once per layer
+    y = w8a8_linear(x, packed)                                      # quantize_act_w8a8 + gemm_w8a8
+    h, q = rms_norm_quantize_w8a8(x, residual, norm_weight, packed) # residual + RMSNorm + quantizer in one pass
+    y = gemm_w8a8(q, packed)
 """
 from __future__ import annotations
 
@@ -115,3 +122,179 @@ def gemm(q: QuantizedAct, packed: PackedWeight, y: torch.Tensor | None = None, s
 def svdq_linear(x: torch.Tensor, packed: PackedWeight, x_tensor_scale=None, stream=None) -> torch.Tensor:
     """One forward of the SVDQ W4A4 linear layer: two launches, no host sync."""
     return gemm(quantize_act(x, packed, x_tensor_scale=x_tensor_scale, stream=stream), packed, stream=stream)
+
+
+# ----------------------------------------------------------------- W8A8 layer
+_DTYPES = {torch.bfloat16: _lib.SVDQ_BF16, torch.float16: _lib.SVDQ_F16, torch.float32: _lib.SVDQ_F32}
+
+
+@dataclass
+class PackedWeightW8A8:
+    N: int
+    K: int
+    w_codes: torch.Tensor               # int8 [N, K]
+    w_scales: torch.Tensor              # fp32 [N]
+    inv_lambda: torch.Tensor | None     # fp32 [K]: 1 / lambda, None without smoothing
+    bias: torch.Tensor | None           # [N], of the output's type
+
+
+@dataclass
+class QuantizedActW8A8:
+    M: int
+    x_codes: torch.Tensor               # int8 [M, K]
+    x_scales: torch.Tensor              # fp32 [M]
+
+
+def _check_tensor(name: str, t: torch.Tensor, dtype, shape: tuple, device) -> None:
+    """What the library cannot see of a contiguous operand behind its pointer."""
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+def _check_rows(name: str, x: torch.Tensor, K: int) -> int:
+    """The library's type of a matrix of activations; rows may be apart, elements of a row not."""
+    if x.dim() != 2 or x.shape[1] != K or x.dtype not in _DTYPES or not x.is_cuda or (K > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name}: expected a CUDA matrix [M, {K}] of bf16, fp16 or fp32 with contiguous rows, got "
+                         f"{x.dtype} {tuple(x.shape)} (strides {x.stride()}) on {x.device}")
+    return _DTYPES[x.dtype]
+
+
+def _row_stride(x: torch.Tensor) -> int:
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _run_on(device, stream, fn, args: tuple, tensors: tuple) -> None:
+    """Calls the binding on `stream` (None: the current one) with `device` current.  The tensors of a call on
+    another stream are marked as in use there, so that the allocator does not hand out their memory early."""
+    if device.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got tensors on {device}")
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            _run_on(device, stream, fn, args, tensors)
+        return
+    current = torch.cuda.current_stream().cuda_stream
+    handle = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
+    fn(*args, handle)
+    if handle != current:
+        used = torch.cuda.ExternalStream(handle, device=device)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(used)
+
+
+def pack_weight_w8a8(W: torch.Tensor, lam: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                     stream=None) -> PackedWeightW8A8:
+    """W [N, K] bf16, fp16 or fp32 -> 8-bit codes and a scale per output channel.  With smoothing divisors
+    lam [K] (fp32) the rows W * lam are quantised and activations are divided by lam."""
+    N, K = W.shape
+    w_type = _check_rows("W", W, K)
+    W = W.contiguous()
+    dev = W.device
+    if lam is not None:
+        _check_tensor("lam", lam, torch.float32, (K,), dev)
+    if bias is not None and (bias.shape != (N,) or bias.dtype not in _DTYPES or bias.device != dev):
+        raise ValueError(f"bias: expected a bf16, fp16 or fp32 tensor of shape ({N},) on {dev}, got {bias.dtype} "
+                         f"{tuple(bias.shape)} on {bias.device}")
+    w_codes = torch.empty(N, K, dtype=torch.int8, device=dev)
+    w_scales = torch.empty(N, dtype=torch.float32, device=dev)
+    inv_lambda = torch.empty(K, dtype=torch.float32, device=dev) if lam is not None else None
+    _run_on(dev, stream, _lib.svdq_pack_weight_w8a8, (w_type, W, N, K, lam, w_codes, w_scales, inv_lambda),
+            (W, lam, w_codes, w_scales, inv_lambda))
+    return PackedWeightW8A8(N, K, w_codes, w_scales, inv_lambda, None if bias is None else bias.contiguous())
+
+
+def alloc_act_w8a8(packed: PackedWeightW8A8, M: int, device) -> QuantizedActW8A8:
+    return QuantizedActW8A8(M, torch.empty(M, packed.K, dtype=torch.int8, device=device),
+                            torch.empty(M, dtype=torch.float32, device=device))
+
+
+def _act_out(packed: PackedWeightW8A8, M: int, device, out: QuantizedActW8A8 | None) -> QuantizedActW8A8:
+    if out is None:
+        return alloc_act_w8a8(packed, M, device)
+    _check_tensor("out.x_codes", out.x_codes, torch.int8, (M, packed.K), device)
+    _check_tensor("out.x_scales", out.x_scales, torch.float32, (M,), device)
+    return out
+
+
+def quantize_act_w8a8(x: torch.Tensor, packed: PackedWeightW8A8, out: QuantizedActW8A8 | None = None,
+                      stream=None) -> QuantizedActW8A8:
+    """x [M, K] bf16, fp16 or fp32 (rows may be apart) -> 8-bit codes and a scale per token."""
+    M, K = x.shape[0], packed.K
+    x_type = _check_rows("x", x, K)
+    dev = x.device
+    if packed.inv_lambda is not None:
+        _check_tensor("packed.inv_lambda", packed.inv_lambda, torch.float32, (K,), dev)
+    q = _act_out(packed, M, dev, out)
+    _run_on(dev, stream, _lib.svdq_quantize_act_w8a8,
+            (x_type, x, _row_stride(x), M, K, packed.inv_lambda, q.x_codes, q.x_scales),
+            (x, packed.inv_lambda, q.x_codes, q.x_scales))
+    return q
+
+
+def rms_norm_quantize_w8a8(x: torch.Tensor, residual: torch.Tensor | None, norm_weight: torch.Tensor | None,
+                           packed: PackedWeightW8A8, eps: float = 1e-6, h_out: torch.Tensor | None = None,
+                           normed: torch.Tensor | None = None, out: QuantizedActW8A8 | None = None,
+                           stream=None) -> tuple[torch.Tensor, QuantizedActW8A8]:
+    """h = x + residual, its RMSNorm, and the 8-bit codes of that: returns (h, codes and scales).  h goes to h_out
+    (a new tensor by default; x or residual itself for an update in place); with residual None and no h_out, h is
+    x.  The normalised rows are also written, in x's type, to `normed` when that is given."""
+    M, K = x.shape[0], packed.K
+    x_type = _check_rows("x", x, K)
+    dev, dt = x.device, x.dtype
+    ldr = K
+    if residual is not None:
+        if _check_rows("residual", residual, K) != x_type or residual.shape[0] != M or residual.device != dev:
+            raise ValueError(f"residual: expected {dt} {(M, K)} on {dev}, got {residual.dtype} "
+                             f"{tuple(residual.shape)} on {residual.device}")
+        ldr = _row_stride(residual)
+    if norm_weight is not None:
+        _check_tensor("norm_weight", norm_weight, dt, (K,), dev)
+    if packed.inv_lambda is not None:
+        _check_tensor("packed.inv_lambda", packed.inv_lambda, torch.float32, (K,), dev)
+    if h_out is not None:
+        _check_tensor("h_out", h_out, dt, (M, K), dev)
+    elif residual is not None:
+        h_out = torch.empty(M, K, dtype=dt, device=dev)
+    if normed is not None:
+        _check_tensor("normed", normed, dt, (M, K), dev)
+    q = _act_out(packed, M, dev, out)
+    _run_on(dev, stream, _lib.svdq_rms_norm_quantize_w8a8,
+            (x_type, x, _row_stride(x), residual, ldr, M, K, norm_weight, eps, packed.inv_lambda, h_out, normed,
+             q.x_codes, q.x_scales),
+            (x, residual, norm_weight, packed.inv_lambda, h_out, normed, q.x_codes, q.x_scales))
+    return (x if h_out is None else h_out), q
+
+
+def gemm_w8a8(q: QuantizedActW8A8, packed: PackedWeightW8A8, y: torch.Tensor | None = None,
+              out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """y [M, N] = x_scales[m] w_scales[n] sum_k codes + bias, in out_dtype (default: y's type, else the bias's,
+    else bf16); the bias has that type too."""
+    M, N, K, dev = q.M, packed.N, packed.K, q.x_codes.device
+    if out_dtype is None:
+        out_dtype = y.dtype if y is not None else packed.bias.dtype if packed.bias is not None else torch.bfloat16
+    if out_dtype not in _DTYPES:
+        raise ValueError(f"out_dtype: expected bf16, fp16 or fp32, got {out_dtype}")
+    _check_tensor("q.x_codes", q.x_codes, torch.int8, (M, K), dev)
+    _check_tensor("q.x_scales", q.x_scales, torch.float32, (M,), dev)
+    _check_tensor("packed.w_codes", packed.w_codes, torch.int8, (N, K), dev)
+    _check_tensor("packed.w_scales", packed.w_scales, torch.float32, (N,), dev)
+    if packed.bias is not None:
+        _check_tensor("packed.bias", packed.bias, out_dtype, (N,), dev)
+    if y is None:
+        y = torch.empty(M, N, dtype=out_dtype, device=dev)
+    else:
+        _check_tensor("y", y, out_dtype, (M, N), dev)
+    _run_on(dev, stream, _lib.svdq_gemm_w8a8,
+            (q.x_codes, q.x_scales, M, packed.w_codes, packed.w_scales, N, K, packed.bias, _DTYPES[out_dtype], y),
+            (q.x_codes, q.x_scales, packed.w_codes, packed.w_scales, packed.bias, y))
+    return y
+
+
+def w8a8_linear(x: torch.Tensor, packed: PackedWeightW8A8, out_dtype: torch.dtype | None = None,
+                stream=None) -> torch.Tensor:
+    """One forward of the W8A8 linear layer: two launches, no host sync.  y is in out_dtype, by default the
+    bias's type or, without one, x's."""
+    if out_dtype is None:
+        out_dtype = packed.bias.dtype if packed.bias is not None else x.dtype
+    return gemm_w8a8(quantize_act_w8a8(x, packed, stream=stream), packed, out_dtype=out_dtype, stream=stream)

@@ -355,6 +355,82 @@ svdq_status svdq_gelu(const void* x, void* y, int64_t n, int approx, svdq_stream
 svdq_status svdq_gemm_w4a16(const void* x, int64_t M, const void* w_codes, const void* w_scales,
                             int64_t N, int64_t K, const void* bias, void* y, svdq_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The 8-bit integer (W8A8) linear layer: the sibling of the 4-bit schemes for
+ * layers whose accuracy 4 bits cost, with the norm that feeds it (no
+ * counterpart on the pages):
+ *     y[m, n] = sx[m] sw[n] sum_k qx[m, k] qw[n, k] + b[n]
+ * qx, qw are signed 8-bit codes (-127..127), sx and sw one fp32 scale per
+ * token and per output channel.  A row t of K values becomes
+ *     a = max |t|,  code = round_half_even(fl(t fl(127 / a))),  scale = fl(a / 127),
+ * in fp32, each step rounded once.  A row with a < 2^-100 gets codes and scale
+ * 0.  A row that holds an infinity or a NaN (or, with the norm, whose sum of
+ * squares overflows fp32) gets codes 0 and scale NaN: its whole row of y, and
+ * no other, is NaN.
+ * Layouts: codes [rows, K] int8, row-major; scales [rows] fp32; K needs no
+ * padding.  Sizes: 1 <= rows < 2^31; 16 <= K < 2^17, K % 16 == 0 (the int32
+ * sum cannot overflow, whatever the codes); N % 8 == 0.
+ * Tensors that are quantised or stored have one of these types: */
+typedef enum { SVDQ_BF16 = 0, SVDQ_F16 = 1, SVDQ_F32 = 2 } svdq_dtype;
+
+/* Offline packing of a W8A8 weight (run once per layer).
+ *   W        device w_type [N, K] (out x in)
+ *   lambda   device fp32 [K] smoothing divisors (> 0 and finite), or NULL: the
+ *            rows t = W lambda are quantised, and activations are to be
+ *            divided by lambda (give inv_lambda to the calls below)
+ * Outputs: w_codes [N, K]; w_scales fp32 [N]; inv_lambda fp32 [K] = 1/lambda
+ *   (not written when lambda is NULL).
+ * Errors: INVALID_ARG (bad type or pointer; lambda without inv_lambda),
+ * UNSUPPORTED_SHAPE (N, K outside the limits above), UNSUPPORTED_DEVICE, CUDA. */
+svdq_status svdq_pack_weight_w8a8(svdq_dtype w_type, const void* W, int64_t N, int64_t K, const float* lambda,
+                                  void* w_codes, float* w_scales, float* inv_lambda, svdq_stream_t stream);
+
+/* Activation quantizer of the W8A8 layer, one kernel, each row read once:
+ * t = x / lambda.
+ *   x           device x_type [M, K], rows ldx elements apart (ldx >= K, a
+ *               multiple of 16 bytes; elements of a row contiguous)
+ *   inv_lambda  device fp32 [K] or NULL (no smoothing)
+ * Outputs: x_codes [M, K], x_scales fp32 [M] (not in x's memory).
+ * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (sizes, ldx), UNSUPPORTED_DEVICE, CUDA. */
+svdq_status svdq_quantize_act_w8a8(svdq_dtype x_type, const void* x, int64_t ldx, int64_t M, int64_t K,
+                                   const float* inv_lambda, void* x_codes, float* x_scales, svdq_stream_t stream);
+
+/* The same behind a residual addition and an RMSNorm, one kernel:
+ *     h = x + residual                             (x when residual is NULL)
+ *     n = h / sqrt(mean_k(h^2) + eps) norm_weight  (weight 1 when NULL)
+ *     codes, scales: the rows t = n / lambda
+ * The row's factor 1 / sqrt(..) enters the scale only: the codes are those of
+ * h fl(norm_weight fl(1/lambda)), and scale = fl(fl(a / 127) / sqrt(..)).
+ * Everything is computed from the fp32 h; the stored h and n are rounded once.
+ *   x, residual  device x_type [M, K], row strides ldx, ldr (as above; ldr is
+ *                not read when residual is NULL)
+ *   norm_weight  device x_type [K] or NULL;   inv_lambda  device fp32 [K] or NULL
+ *   eps          0 < eps < 1
+ * Outputs (contiguous, device; each may be NULL except as said):
+ *   h_out    x_type [M, K]: the new residual stream; may be x or residual
+ *            itself (in place, that one's row stride being K)
+ *   normed   x_type [M, K]: n, for layers that read it in 16 or 32 bits (for
+ *            example svdq_quantize_act)
+ *   x_codes [M, K], x_scales fp32 [M]: both or neither; at least one of
+ *   {codes and scales, normed} must be given.
+ * Errors: INVALID_ARG (pointers, eps, outputs that overlap each other or an
+ * input other than as h_out in place), UNSUPPORTED_SHAPE (sizes, strides),
+ * UNSUPPORTED_DEVICE, CUDA. */
+svdq_status svdq_rms_norm_quantize_w8a8(svdq_dtype x_type, const void* x, int64_t ldx, const void* residual,
+                                        int64_t ldr, int64_t M, int64_t K, const void* norm_weight, float eps,
+                                        const float* inv_lambda, void* h_out, void* normed, void* x_codes,
+                                        float* x_scales, svdq_stream_t stream);
+
+/* The W8A8 GEMM, y = round(fl(fl(float(sum) sx) sw + b)): the sum exact in
+ * int32, one rounding to y's type at the end.  Inputs are the outputs of the
+ * calls above; bias is device y_type [N] or NULL.  Output: y device y_type
+ * [M, N], contiguous.  One kernel; no workspace; results do not depend on how
+ * the work was split.  Errors: INVALID_ARG, UNSUPPORTED_SHAPE,
+ * UNSUPPORTED_DEVICE, CUDA. */
+svdq_status svdq_gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, const void* w_codes,
+                           const float* w_scales, int64_t N, int64_t K, const void* bias, svdq_dtype y_type, void* y,
+                           svdq_stream_t stream);
+
 /* Offline split of a layer's weight into the low-rank branch and the residual
  * that svdq_pack_weight quantizes (the SVDQuant decomposition the Diffusers
  * docs page "Nunchaku Lite" builds on; the tutorial's offline quantization
@@ -397,7 +473,8 @@ svdq_status svdq_device_status(int clear, int* site);
  *    major.minor (major = -1 removes the override), to test the device check.
  *  svdq_debug_force_gemm_tiles: choose the nvfp4 GEMM kernel: 0 = automatic
  *    (M <= 128: 128 x 256 tiles on single CTAs; M > 128: CTA-pair tiles),
- *    1 = always single CTAs, 2 = always CTA pairs.  Both kernels compute the
+ *    1 = always single CTAs, 2 = always CTA pairs; the same for the W8A8
+ *    GEMM (automatic: by its tile counts).  Both kernels compute the
  *    same y; this exists so that tests can run each on the same inputs.  Any
  *    other value is SVDQ_ERR_INVALID_ARG. */
 svdq_status svdq_debug_set_wait_limit_ns(uint64_t ns);

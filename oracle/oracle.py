@@ -401,3 +401,54 @@ def svdq_linear(precision: str, x_bits, lam, R_bits, L_down_bits, L_up_bits, bia
             res.y, res.y_bf16 = int4_linear(xc, xsc, wc, wsc, L, L_up_bits, bias_bits, rows)
         return res
     raise ValueError(precision)
+
+
+# ------------------------------------------------------------- W8A8 (8-bit integer) layer
+# Plain numpy: the codes' definition is in fp32 steps (each numpy fp32 operation
+# rounds once), everything else in fp64.
+W8_TINY = 2.0 ** -100
+
+
+def w8a8_quantize_rows(t: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
+    """fp32 rows t [M, K] -> (int8 codes [M, K], fp32 scales [M]): a = max|t|,
+    code = round_half_even(fl(t fl(127 / a))), scale = fl(a / 127); rows with
+    a < 2^-100 are zero, rows with a value that is not finite get scale NaN."""
+    t = np.asarray(t, np.float32)
+    codes = np.zeros(t.shape, np.int8)
+    scales = np.zeros(t.shape[0], np.float32)
+    for m, row in enumerate(t):
+        if not np.isfinite(row).all():
+            scales[m] = np.nan
+            continue
+        a = np.float32(np.abs(row).max())
+        if a < W8_TINY:
+            continue
+        codes[m] = np.rint(row * (np.float32(127) / a)).astype(np.int8)
+        scales[m] = a / np.float32(127)
+    return codes, scales
+
+
+def w8a8_norm_rows(x: np.ndarray, residual, weight, inv_lambda) -> tuple[np.ndarray, np.ndarray]:
+    """(h, t) in fp32: h = fl(x + residual), t = fl(h fl(weight inv_lambda))."""
+    h = np.asarray(x, np.float32)
+    if residual is not None:
+        h = h + np.asarray(residual, np.float32)
+    gain = np.ones(h.shape[1], np.float32)
+    if weight is not None:
+        gain = gain * np.asarray(weight, np.float32)
+    if inv_lambda is not None:
+        gain = gain * np.asarray(inv_lambda, np.float32)
+    return h, h * gain
+
+
+def w8a8_rstd(h: np.ndarray, eps: float) -> np.ndarray:
+    """1 / sqrt(mean_k h^2 + eps) of each row, fp64."""
+    h = np.asarray(h, np.float64)
+    return 1.0 / np.sqrt((h * h).mean(axis=1) + eps)
+
+
+def w8a8_gemm(x_codes, x_scales, w_codes, w_scales, bias=None) -> np.ndarray:
+    """The scaled product in fp64 (whole-number sums below 2^53 are exact)."""
+    acc = np.asarray(x_codes, np.float64) @ np.asarray(w_codes, np.float64).T
+    y = acc * np.asarray(x_scales, np.float64)[:, None] * np.asarray(w_scales, np.float64)
+    return y if bias is None else y + np.asarray(bias, np.float64)
