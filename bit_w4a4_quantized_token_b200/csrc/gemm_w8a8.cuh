@@ -28,7 +28,6 @@ struct GemmW8Args {
     int last_steps;          // 32-byte K-steps of the last chunk (1..4)
     int m_tiles, n_tiles;
     int stages;              // narrow kernel: ring depth
-    int out;                 // type of y and bias: kBf16, kF16 or kF32
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T with signed 8-bit integers, s32 accumulate, on a CTA pair.
@@ -65,11 +64,12 @@ enum : uint32_t {
 namespace w8p {
 constexpr int BM = 256;                       // tokens of a tile (128 per CTA)
 constexpr int BN = 256;                       // output channels of a tile (128 weight rows loaded per CTA)
-constexpr int BK = 128;                       // bytes of K per stage
-constexpr int kStages = 6;
-constexpr int A_BYTES = 128 * BK;
+constexpr int BK = 128;                       // bytes of K of a chunk: the rows of a swizzled box
+constexpr int kPer = 2;                       // chunks per stage
+constexpr int kStages = 3;
+constexpr int A_BYTES = 128 * BK;             // of one chunk
 constexpr int B_BYTES = 128 * BK;
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int STAGE_BYTES = kPer * (A_BYTES + B_BYTES);
 constexpr int kWarpX = 0, kWarpW = 1, kWarpMma = 2, kWarpAlloc = 3;   // roles of warps 0..3
 constexpr int kEpiWarp0 = 4;
 constexpr int kEpiWarps = 8;                  // two per TMEM lane quarter, 128 columns each
@@ -144,6 +144,14 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // the first weight stages on their way into the L2 while the previous
+    // kernel ends (only into the L2: that kernel may have written them)
+    if (warp >= (uint32_t)kEpiWarp0 && lane == 0) {
+        int m, n;
+        w8_tile(cluster, a.m_tiles, a.n_tiles, m, n);
+        const int c = (int)warp - kEpiWarp0;
+        if (c < min(a.chunks, kStages * kPer)) tma_prefetch_l2_2d(&tm_w, c * BK, n * BN + 128 * (int)rank);
+    }
     griddep_wait();   // everything above overlaps the end of the previous kernel
 
     if (warp == kWarpX || warp == kWarpW) {
@@ -153,23 +161,30 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
         if (lane == 0) {
             const bool is_x = warp == kWarpX;
             const CUtensorMap* map = is_x ? &tm_x : &tm_w;
-            int it = 0;
+            int s = 0;
+            uint32_t ph = 1u;
             bool ok = true;
             for (int id = cluster; id < total && ok; id += n_clusters) {
                 int m, n;
                 w8_tile(id, a.m_tiles, a.n_tiles, m, n);
                 const int row0 = (is_x ? m * BM : n * BN) + 128 * (int)rank;
-                for (int c = 0; c < a.chunks; ++c, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait(&empty[s], ((uint32_t)(it / kStages) & 1u) ^ 1u, kSiteW8Empty)) {
+                for (int c = 0; c < a.chunks; c += kPer) {
+                    if (!bounded_wait(&empty[s], ph, kSiteW8Empty)) {
                         s_failed = 1;
                         ok = false;
                         break;
                     }
-                    uint8_t* dst = smem + (size_t)s * STAGE_BYTES + (is_x ? 0 : A_BYTES);
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * A_BYTES);
-                    tma_load_2d_pair(dst, map, cluster_addr(&full[s], 0), c * BK, row0);
+                    uint8_t* dst = smem + (size_t)s * STAGE_BYTES + (is_x ? 0 : kPer * A_BYTES);
+                    const uint32_t bar = cluster_addr(&full[s], 0);
+                    const bool both = c + 1 < a.chunks;
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], both ? 4u * A_BYTES : 2u * A_BYTES);
+                    tma_load_2d_pair(dst, map, bar, c * BK, row0);
+                    if (both) tma_load_2d_pair(dst + A_BYTES, map, bar, (c + 1) * BK, row0);
                     if (is_x) s_issued[s] = s_issued[s] + 1;
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
             }
         }
@@ -178,29 +193,42 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = idesc_m(idesc_s8_s32(BN), BM);
             const uint32_t smem0 = smem_u32(smem);
-            int it = 0, local = 0;
+            int s = 0, local = 0;
+            uint32_t ph = 0u;
             bool ok = true;
             for (int id = cluster; id < total && ok; id += n_clusters, ++local) {
                 const uint32_t acc = tmem + (uint32_t)(local & 1) * ACC_COLS;
-                if (!mbar_wait(&acc_empty[local & 1], ((uint32_t)(local >> 1) & 1u) ^ 1u, kSiteW8AccEmpty)) {
+                if (!bounded_wait(&acc_empty[local & 1], ((uint32_t)(local >> 1) & 1u) ^ 1u, kSiteW8AccEmpty)) {
                     s_failed = 1;
                     break;
                 }
-                for (int c = 0; c < a.chunks; ++c, ++it) {
-                    const int s = it % kStages;
-                    if (!mbar_wait(&full[s], (uint32_t)(it / kStages) & 1u, kSiteW8Full)) {
+                for (int c = 0; c < a.chunks; c += kPer) {
+                    if (!bounded_wait(&full[s], ph, kSiteW8Full)) {
                         s_failed = 1;
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t sa = smem0 + (uint32_t)s * STAGE_BYTES;
-                    const uint64_t da = desc_sw128(sa), db = desc_sw128(sa + A_BYTES);   // + 2 per 32-byte K-step
-                    const int steps = c + 1 < a.chunks ? 4 : a.last_steps;
+                    const uint64_t da = desc_sw128(sa), db = desc_sw128(sa + kPer * A_BYTES);
+                    const uint32_t more = c > 0 ? 1u : 0u;
+                    // K-step j of the stage: 32 bytes of K, 2 descriptor units apart inside a chunk
+                    const auto mma = [&](int j) {
+                        mma_s8_pair(acc, da + (uint64_t)(j >> 2) * (A_BYTES >> 4) + 2u * (j & 3),
+                                    db + (uint64_t)(j >> 2) * (B_BYTES >> 4) + 2u * (j & 3), idesc, j == 0 ? more : 1u);
+                    };
+                    if (c + kPer < a.chunks || (c + kPer == a.chunks && a.last_steps == 4)) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (j < steps) mma_s8_pair(acc, da + 2u * j, db + 2u * j, idesc, (c > 0 || j > 0) ? 1u : 0u);
+                        for (int j = 0; j < 4 * kPer; ++j) mma(j);
+                    } else {   // the end of K inside a stage
+                        const int n_steps = 4 * (a.chunks - c - 1) + a.last_steps;
+                        for (int j = 0; j < n_steps; ++j) mma(j);
+                    }
                     tc_commit_pair(&empty[s], 0x3);
+                    if (++s == kStages) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
                 }
                 if (ok) tc_commit_pair(&acc_full[local & 1], 0x3);
             }
@@ -211,8 +239,8 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
         const int half = (int)(e >> 2);
         float* col_s = reinterpret_cast<float*>(smem + COL_OFF + (size_t)e * 2 * kColBytes);
         float* col_b = col_s + 128;
-        const uint32_t box = smem_u32(smem + BOX_OFF) + e * (uint32_t)kBoxBytes;
-        constexpr int kBoxCols = OUT == kF32 ? 16 : 32;
+        constexpr int kBoxCols = OUT == kF32 ? 16 : 32, kBoxes = 128 / kBoxCols;
+        static_assert(kEpiWarps * kBoxes * kBoxBytes <= BAR_OFF, "the last tile's boxes do not fit in the ring");
         int local = 0;
         for (int id = cluster; id < total; id += n_clusters, ++local) {
             int mt, nt;
@@ -230,40 +258,52 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
             }
             const float sx = row < a.M ? a.x_scales[row] : 0.0f;
             __syncwarp();
-            if (!mbar_wait(&acc_full[local & 1], (uint32_t)(local >> 1) & 1u, kSiteW8Acc)) {
+            if (!bounded_wait(&acc_full[local & 1], (uint32_t)(local >> 1) & 1u, kSiteW8Acc)) {
                 s_failed = 1;
                 break;
             }
             tc_fence_after();
             const uint32_t acc = tmem + ((32u * q) << 16) + (uint32_t)(local & 1) * ACC_COLS + 128u * (uint32_t)half;
+            // The main loop hides the epilogue of every tile but the last.
+            // There each box has its own place in the ring, which is drained
+            // by now, so that no box waits for the store of another.
+            const bool last = id + n_clusters >= total;
+            if (last) griddep_launch_dependents();
+            const uint32_t box0 = last ? smem_u32(smem) + e * (uint32_t)(kBoxes * kBoxBytes)
+                                       : smem_u32(smem + BOX_OFF) + e * (uint32_t)kBoxBytes;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(acc, v);
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(acc + 32u * c, v);
+                float o[32];
                 tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = (float)(int)v[i];
+                // the next columns are on their way while these are scaled and stored
+                if (c < 3) tmem_ld_32x32b_x32(acc + 32u * (c + 1), v);
                 if (c == 3) {   // drained: the accumulator may be overwritten
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(cluster_addr(&acc_empty[local & 1], 0));
                 }
                 if (n0 + 32 * c >= a.N) continue;   // warp-uniform
-                float o[32];
 #pragma unroll
                 for (int i = 0; i < 32; i += 4) {
                     const float4 s4 = *reinterpret_cast<const float4*>(col_s + 32 * c + i);
                     const float4 b4 = *reinterpret_cast<const float4*>(col_b + 32 * c + i);
-                    float f0 = (float)(int)v[i], f1 = (float)(int)v[i + 1];
-                    float f2 = (float)(int)v[i + 2], f3 = (float)(int)v[i + 3];
-                    fmul2_rn(f0, f1, sx, sx, f0, f1);
-                    fmul2_rn(f2, f3, sx, sx, f2, f3);
-                    ffma2_rn(f0, f1, s4.x, s4.y, b4.x, b4.y, o[i], o[i + 1]);
-                    ffma2_rn(f2, f3, s4.z, s4.w, b4.z, b4.w, o[i + 2], o[i + 3]);
+                    fmul2_rn(o[i], o[i + 1], sx, sx, o[i], o[i + 1]);
+                    fmul2_rn(o[i + 2], o[i + 3], sx, sx, o[i + 2], o[i + 3]);
+                    ffma2_rn(o[i], o[i + 1], s4.x, s4.y, b4.x, b4.y, o[i], o[i + 1]);
+                    ffma2_rn(o[i + 2], o[i + 3], s4.z, s4.w, b4.z, b4.w, o[i + 2], o[i + 3]);
                 }
 #pragma unroll
                 for (int p = 0; p < 32 / kBoxCols; ++p) {
                     // 32 rows x 64 bytes through the warp's box (64-byte swizzle), stored with TMA
-                    if (lane == 0) bulk_wait_group_read<0>();
-                    __syncwarp();
+                    const uint32_t box = last ? box0 + (uint32_t)((c * 32 / kBoxCols + p) * kBoxBytes) : box0;
+                    if (!last) {
+                        if (lane == 0) bulk_wait_group_read<0>();
+                        __syncwarp();
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t w[4];
@@ -298,7 +338,7 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
         // exits (best effort: each wait is bounded)
         for (int s = 0; s < kStages; ++s) {
             const int n = *reinterpret_cast<volatile int*>(&s_issued[s]);
-            if (n > 0) mbar_wait(&full[s], (uint32_t)(n - 1) & 1u, kSiteW8Drain);
+            if (n > 0) bounded_wait(&full[s], (uint32_t)(n - 1) & 1u, kSiteW8Drain);
         }
     }
     tc_fence_before();
@@ -313,47 +353,82 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
 namespace w8n {
 constexpr int BN = 128;                       // output channels of a tile: the MMA's M
 constexpr int BK = 128;
-constexpr int W_BYTES = BN * BK;
-constexpr int kMaxStages = 16;
+// Chunks of K per stage: two where the tokens add little to a stage's bytes
+// (one barrier round trip for both), one where two would leave the ring with
+// two stages.
+__host__ __device__ constexpr int per(int nt) { return nt <= 64 ? 2 : 1; }
+constexpr int W_BYTES = BN * BK;              // of one chunk
+constexpr int kMaxStages = 8;
 constexpr int kMaxSplit = 8;                  // CTAs of a cluster that share a tile's K range
-constexpr int kThreads = 192;                 // warp 0: loads, warp 1: MMAs, warps 2..5: epilogue
+constexpr int kEpiWarps = 8;                  // two per TMEM lane quarter, taking turns of 16 tokens
+// A thread issues a TMA load about every 300 cycles whatever the size of its
+// box, so three share the loads: two take turns with the weight boxes, one
+// loads the token boxes.
+constexpr int kWarpW0 = 0, kWarpW1 = 1, kWarpX = 2;
+// Two warps issue the MMAs of alternate stages into an accumulator each (the
+// epilogue adds the two, exactly): one thread needs ~1000 cycles for the wait,
+// the eight MMAs and the commit of a stage, which held a CTA below 40 bytes of
+// weights a cycle.
+constexpr int kWarpMma0 = 3, kWarpMma1 = 4, kEpiWarp0 = 5;
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBarBytes = 512;
 static_assert((2 * kMaxStages + 1) * 8 + 4 <= kBarBytes, "barriers do not fit");
-__host__ __device__ constexpr int stage_bytes(int nt) { return W_BYTES + nt * BK; }
-// barriers, token scales, alignment slack
-__host__ __device__ constexpr int fixed_bytes(int nt) { return 1024 + kBarBytes + nt * 4; }
-// int32 partial sums of a tile, kept in the ring once it has been drained
-__host__ __device__ constexpr int partial_bytes(int nt) { return BN * nt * 4; }
+__host__ __device__ constexpr int stage_bytes(int nt) { return per(nt) * (W_BYTES + nt * BK); }
+// int32 partial sums that a CTA receives: for each of its tokens (every
+// split-th of the tile) 128 channels from every CTA of the cluster
+__host__ __device__ constexpr int partial_bytes(int nt, int split) {
+    return split == 1 ? 0 : (nt + split - 1) / split * split * BN * 4;
+}
+// alignment slack, barriers, token scales, partial sums
+__host__ __device__ constexpr int fixed_bytes(int nt, int split) {
+    return 1024 + kBarBytes + nt * 4 + partial_bytes(nt, split);
+}
 }  // namespace w8n
 
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ uint32_t cluster_addr_u32(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
 }
+__device__ __forceinline__ void st_cluster_s32(uint32_t addr, int v) {
+    asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void store_out(void* y, int out, int64_t i, float v) {
-    if (out == kF32)
-        reinterpret_cast<float*>(y)[i] = v;
-    else if (out == kF16)
-        reinterpret_cast<__half*>(y)[i] = __float2half_rn(v);
-    else
-        reinterpret_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
-}
+template <int OUT>
+struct OutType {
+    using type = __nv_bfloat16;
+    __device__ static __nv_bfloat16 of(float v) { return __float2bfloat16_rn(v); }
+};
+template <>
+struct OutType<kF16> {
+    using type = __half;
+    __device__ static __half of(float v) { return __float2half_rn(v); }
+};
+template <>
+struct OutType<kF32> {
+    using type = float;
+    __device__ static float of(float v) { return v; }
+};
 
 // The product transposed: the MMA's A operand (M = 128) holds weight rows, its
 // B operand NT token rows, so that few tokens cost few tensor-core columns and
 // few bytes of TMEM, and the weight streams through a ring as deep as shared
-// memory allows.  The cluster's CTAs split the K range; their int32 partial
-// sums meet in shared memory (exact, so the split does not change y), and each
-// CTA finishes a share of the tile's tokens.
-template <int NT>
+// memory allows.  The cluster's CTAs split the K range; each sends the int32
+// partial sums of a token to the CTA that owns it (token i of the tile: CTA
+// i mod split), which adds them (exact, so the split does not change y),
+// scales and stores.
+template <int NT, int OUT>
 __global__ void __launch_bounds__(w8n::kThreads)
     gemm_w8a8_narrow_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                             GemmW8Args a) {
     using namespace w8n;
+    constexpr int kPer = per(NT);
     constexpr int STAGE = stage_bytes(NT);
-    constexpr uint32_t TCOLS = NT < 32 ? 32 : NT;
+    constexpr uint32_t TCOLS = 2 * NT;   // two accumulators
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + (size_t)a.stages * STAGE);
@@ -361,30 +436,29 @@ __global__ void __launch_bounds__(w8n::kThreads)
     uint64_t* acc_full = empty + kMaxStages;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
     float* s_sx = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(full) + kBarBytes);
-    int* s_part = reinterpret_cast<int*>(smem);
+    int* s_part = reinterpret_cast<int*>(s_sx + NT);   // [own token][source CTA][128 channels]
     __shared__ int s_failed;
     __shared__ int s_issued;
 
     const uint32_t warp = warp_id(), lane = lane_id();
-    const int split = (int)gridDim.x, rank = (int)blockIdx.x;   // the cluster is the whole x extent
+    // the cluster is the whole x extent, a power of two
+    const int split = (int)gridDim.x, rank = (int)blockIdx.x, log_split = 31 - __clz(split);
     const int n0 = (int)blockIdx.y * BN, m0 = (int)blockIdx.z * NT;
     const int c0 = (int)((int64_t)a.chunks * rank / split), c1 = (int)((int64_t)a.chunks * (rank + 1) / split);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < a.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], kPer + 1);   // the loading warps that fill it
             mbar_init(&empty[s], 1);
         }
-        mbar_init(acc_full, 1);
+        mbar_init(acc_full, 2);       // both MMA warps
         s_failed = 0;
         s_issued = 0;
         fence_barrier_init();
     }
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tm_x);
-        prefetch_tensormap(&tm_w);
-    }
-    if (warp == 1) {
+    if (warp == kWarpW0 && lane == 0) prefetch_tensormap(&tm_w);
+    if (warp == kWarpX && lane == 0) prefetch_tensormap(&tm_x);
+    if (warp == kWarpMma0) {
         tmem_alloc(tmem_slot, TCOLS);
         tmem_relinquish();
     }
@@ -392,119 +466,182 @@ __global__ void __launch_bounds__(w8n::kThreads)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // Decode: the ring's worth of weights on its way into the L2 while the
+    // previous kernel ends (only into the L2: that kernel may have written
+    // them).  Quantizer and GEMM of one token: 20.5 -> 19.8 us at N = 10240,
+    // K = 8192; with more tokens (37, N = 11008, K = 2080) 9.9 -> 10.7 us.
+    if (NT == 16 && warp >= (uint32_t)kEpiWarp0 && lane == 0)
+        for (int c = c0 + (int)warp - kEpiWarp0; c < min(c1, c0 + a.stages * kPer); c += kEpiWarps)
+            tma_prefetch_l2_2d(&tm_w, c * BK, n0);
     griddep_wait();
+    griddep_launch_dependents();
+    if (split > 1) cluster_arrive();   // waited for before the first remote store: every CTA has started by then
 
     float sw = 0.0f, bias = 0.0f;
-    const int q = (int)(warp & 3u);
-    const int n = n0 + 32 * q + (int)lane;   // an epilogue thread's output channel
-    if (warp == 0) {
+    using T = typename OutType<OUT>::type;
+    const int q = (int)(warp & 3u), part = ((int)warp - kEpiWarp0) >> 2;   // an epilogue warp's lane quarter, its turn
+    const int n = n0 + 32 * q + (int)lane;                          // an epilogue thread's output channel
+    const int tokens = min(NT, a.M - m0);
+    // A stage is kPer chunks of the weight tile, then kPer of the token tile.
+    if (warp <= kWarpX) {
         if (lane == 0) {
-            for (int c = c0; c < c1; ++c) {
-                const int it = c - c0, s = it % a.stages;
-                if (!mbar_wait(&empty[s], ((uint32_t)(it / a.stages) & 1u) ^ 1u, kSiteW8NarrowEmpty)) {
+            int s = 0;
+            uint32_t ph = 1u;
+            for (int c = c0, it = 0; c < c1; c += kPer, ++it) {
+                // with one chunk per stage the weight warps take alternate
+                // stages (always the same ones: the ring's length is even)
+                const bool mine = kPer == 2 || warp == kWarpX || (it & 1) == (int)warp;
+                if (mine && !bounded_wait(&empty[s], ph, kSiteW8NarrowEmpty)) {
                     s_failed = 1;
                     break;
                 }
                 uint8_t* dst = smem + (size_t)s * STAGE;
-                mbar_arrive_expect_tx(&full[s], (uint32_t)STAGE);
-                tma_load_2d(dst, &tm_w, &full[s], c * BK, n0);
-                tma_load_2d(dst + W_BYTES, &tm_x, &full[s], c * BK, m0);
-                s_issued = it + 1;
+                if (warp == kWarpX) {
+                    const bool both = kPer == 2 && c + 1 < c1;
+                    mbar_arrive_expect_tx(&full[s], (uint32_t)(NT * BK) * (both ? 2u : 1u));
+                    tma_load_2d(dst + kPer * W_BYTES, &tm_x, &full[s], c * BK, m0);
+                    if (both) tma_load_2d(dst + kPer * W_BYTES + NT * BK, &tm_x, &full[s], (c + 1) * BK, m0);
+                    s_issued = s_issued + 1;
+                } else if (mine) {
+                    const int k = kPer == 2 ? (int)warp : 0;   // the chunk of the stage
+                    if (c + k < c1) {
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)W_BYTES);
+                        tma_load_2d(dst + k * W_BYTES, &tm_w, &full[s], (c + k) * BK, n0);
+                    } else {
+                        mbar_arrive(&full[s]);   // a last stage of one chunk
+                    }
+                }
+                if (++s == a.stages) {
+                    s = 0;
+                    ph ^= 1u;
+                }
             }
         }
-    } else if (warp == 1) {
+        __syncwarp();
+        if (split > 1) cluster_wait();
+    } else if (warp <= kWarpMma1) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_s8_s32(NT);
             const uint32_t smem0 = smem_u32(smem);
+            const int me = (int)warp - kWarpMma0;
+            const uint32_t acc = tmem + (uint32_t)(me * NT);
             bool ok = true;
-            for (int c = c0; c < c1; ++c) {
-                const int it = c - c0, s = it % a.stages;
-                if (!mbar_wait(&full[s], (uint32_t)(it / a.stages) & 1u, kSiteW8NarrowFull)) {
+            int s = me;
+            uint32_t ph = 0u;
+            for (int c = c0 + me * kPer; c < c1; c += 2 * kPer, s += 2) {
+                for (; s >= a.stages; s -= a.stages) ph ^= 1u;
+                if (!bounded_wait(&full[s], ph, kSiteW8NarrowFull)) {
                     s_failed = 1;
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t sa = smem0 + (uint32_t)s * (uint32_t)STAGE;
-                const uint64_t da = desc_sw128(sa), db = desc_sw128(sa + W_BYTES);
-                const int steps = c + 1 < a.chunks ? 4 : a.last_steps;
+                const uint64_t da = desc_sw128(sa), db = desc_sw128(sa + (uint32_t)(kPer * W_BYTES));
+                constexpr uint64_t kNextW = W_BYTES >> 4, kNextX = (NT * BK) >> 4;   // descriptor units per chunk
+                const uint32_t more = c > c0 + me * kPer ? 1u : 0u;
+                const auto mma = [&](int j) {   // K-step j of the stage
+                    mma_s8(acc, da + (uint64_t)(j >> 2) * kNextW + 2u * (j & 3),
+                           db + (uint64_t)(j >> 2) * kNextX + 2u * (j & 3), idesc, j == 0 ? more : 1u);
+                };
+                const int here = min(kPer, c1 - c);
+                if (here == kPer && (c + kPer < a.chunks || a.last_steps == 4)) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < steps) mma_s8(tmem, da + 2u * j, db + 2u * j, idesc, (it > 0 || j > 0) ? 1u : 0u);
+                    for (int j = 0; j < 4 * kPer; ++j) mma(j);
+                } else {   // a stage that is not full, or that ends K inside a chunk
+                    const int n_steps = 4 * here - (c + here == a.chunks ? 4 - a.last_steps : 0);
+                    for (int j = 0; j < n_steps; ++j) mma(j);
+                }
                 tc_commit(&empty[s]);
             }
             if (ok) tc_commit(acc_full);
         }
+        __syncwarp();
+        if (split > 1) cluster_wait();
     } else {
-        const int t = (int)threadIdx.x - 64;
-        for (int i = t; i < NT; i += 128) s_sx[i] = m0 + i < a.M ? a.x_scales[m0 + i] : 0.0f;
+        const int t = (int)threadIdx.x - 32 * kEpiWarp0;
+        for (int i = t; i < NT; i += 32 * kEpiWarps) s_sx[i] = i < tokens ? a.x_scales[m0 + i] : 0.0f;
         if (n < a.N) {
             sw = a.w_scales[n];
-            bias = bias_at(a.bias, a.out, n);
+            bias = bias_at(a.bias, OUT, n);
         }
-        named_bar_sync(1, 128);   // the token scales are in shared memory
-        if (!mbar_wait(acc_full, 0u, kSiteW8NarrowAcc)) s_failed = 1;
+        named_bar_sync(1, 32 * kEpiWarps);   // the token scales are in shared memory
+        if (split > 1) cluster_wait();
+        if (!bounded_wait(acc_full, 0u, kSiteW8NarrowAcc)) s_failed = 1;
         tc_fence_after();
+        __syncwarp();
         const uint32_t acc = tmem + ((32u * (uint32_t)q) << 16);
-        if (split == 1) {
-            if (!*reinterpret_cast<volatile int*>(&s_failed)) {
 #pragma unroll 1
-                for (int c = 0; c < NT; c += 16) {
-                    if (m0 + c >= a.M) break;
-                    uint32_t v[16];
-                    __syncwarp();
-                    tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
-                    tmem_ld_wait();
-                    if (n < a.N) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (m0 + c + i < a.M)
-                                store_out(a.y, a.out, (int64_t)(m0 + c + i) * a.N + n,
-                                          fmaf(__fmul_rn((float)(int)v[i], s_sx[c + i]), sw, bias));
-                    }
-                }
-            }
-        } else {
-            // the ring is drained: every load has been consumed by an MMA that acc_full waited for
-#pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
-                if (m0 + c >= a.M) break;
-                uint32_t v[16];
-                __syncwarp();
-                tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
+        for (int c = 16 * part; c < tokens; c += 32) {
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(acc + (uint32_t)c, v);
+            if (c1 - c0 > kPer) {   // the second MMA warp had stages too
+                uint32_t u[16];
+                tmem_ld_32x32b_x16(acc + (uint32_t)(NT + c), u);
                 tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) s_part[(c + i) * BN + 32 * q + (int)lane] = (int)v[i];
+                for (int i = 0; i < 16; ++i) v[i] += u[i];
+            }
+            tmem_ld_wait();
+            if (split == 1) {
+                if (n < a.N) {
+                    T* y = reinterpret_cast<T*>(a.y) + (int64_t)(m0 + c) * a.N + n;
+                    T o[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[i] = OutType<OUT>::of(fmaf(__fmul_rn((float)(int)v[i], s_sx[c + i]), sw, bias));
+                    if (c + 16 <= tokens) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, y += a.N) *y = o[i];
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i, y += a.N)
+                            if (c + i < tokens) *y = o[i];
+                    }
+                }
+            } else {
+                const uint32_t mine = smem_u32(s_part) + (uint32_t)(rank * BN + 32 * q + (int)lane) * 4u;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int tok = c + i;
+                    if (tok < tokens)
+                        st_cluster_s32(cluster_addr_u32(mine + (uint32_t)((tok >> log_split) << log_split) * BN * 4u,
+                                                        (uint32_t)(tok & (split - 1))),
+                                       (int)v[i]);
+                }
             }
         }
     }
     __syncwarp();
     if (split > 1) {
-        cluster_sync_all();   // every CTA's partial sums are in its shared memory
-        if (warp >= 2 && n < a.N) {
-            const int tokens = min(NT, a.M - m0);
-            const uint32_t mine = (uint32_t)(32 * q + (int)lane) * 4u;
-            for (int i = rank; i < tokens; i += split) {
+        cluster_sync_all();   // every partial sum has arrived
+        if (warp >= (uint32_t)kEpiWarp0 && n < a.N) {
+            // own token j (token rank + j split of the tile): [j][source CTA][channel]
+            const int* mine = s_part + 32 * q + (int)lane;
+            T* y = reinterpret_cast<T*>(a.y) + (int64_t)(m0 + rank) * a.N + n;
+            const int own = tokens > rank ? ((tokens - rank - 1) >> log_split) + 1 : 0;
+#pragma unroll 2
+            for (int j = part; j < own; j += 2) {
                 int sum = 0;
-                for (int r = 0; r < split; ++r)
-                    sum += ld_cluster_s32(cluster_addr(s_part, (uint32_t)r) + (uint32_t)(i * BN) * 4u + mine);
-                store_out(a.y, a.out, (int64_t)(m0 + i) * a.N + n, fmaf(__fmul_rn((float)sum, s_sx[i]), sw, bias));
+#pragma unroll
+                for (int r = 0; r < kMaxSplit; ++r)
+                    if (r < split) sum += mine[((j << log_split) + r) * BN];
+                y[(int64_t)(j << log_split) * a.N] =
+                    OutType<OUT>::of(fmaf(__fmul_rn((float)sum, s_sx[rank + (j << log_split)]), sw, bias));
             }
         }
-        __syncwarp();
-        cluster_sync_all();   // no CTA's partial sums go away while another reads them
     }
     __syncthreads();
     if (s_failed && warp == 0 && lane == 0) {
         // after a timeout, let the loads already issued land (best effort: each wait is bounded)
         for (int s = 0; s < a.stages; ++s) {
             const int issued = *reinterpret_cast<volatile int*>(&s_issued);
-            if (issued > s) mbar_wait(&full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1u, kSiteW8NarrowDrain);
+            if (issued > s) bounded_wait(&full[s], (uint32_t)((issued - 1 - s) / a.stages) & 1u, kSiteW8NarrowDrain);
         }
     }
     __syncthreads();
     tc_fence_before();
-    if (warp == 1) {
+    if (warp == kWarpMma0) {
         tc_fence_after();
         tmem_dealloc(tmem, TCOLS);
     }

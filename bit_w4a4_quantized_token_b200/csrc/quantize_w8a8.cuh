@@ -28,6 +28,19 @@
 #include "sm100_ptx.cuh"
 
 namespace svdq {
+
+// Wait for the phase with the given parity; false after the wait limit.  The
+// first tries only suspend in the hardware: reading the timer and the limit
+// from memory costs hundreds of cycles, which a wait that ends soon must not
+// pay (a wait of every stage that paid them bounded the 128 x 64 tiles of the
+// W8A8 GEMM at ~900 cycles a stage).
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, uint32_t site) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_timed(bar, parity, site);
+}
+
 namespace q8 {
 constexpr int kMaxThreads = 512;     // of the register-resident kernel
 constexpr int kTwoPassThreads = 1024;
@@ -169,18 +182,19 @@ __device__ __forceinline__ RowFactors row_factors(uint32_t abits, float ss, int 
     return f;
 }
 
-// Maximum of abits and sum of ss over the block; `slot` holds one entry per
-// warp and is not written again before the block's next barrier but one.
+// Maximum of abits and sum of ss over a group of warps of the block (this one
+// is number `warp` of threads / 32); `slot` holds one entry per warp and is not
+// written again before the group's next barrier but one.
 template <bool NORM>
-__device__ __forceinline__ void block_reduce(uint32_t& abits, float& ss, uint2* slot) {
+__device__ __forceinline__ void group_reduce(uint32_t& abits, float& ss, uint2* slot, int warp, int threads) {
     abits = __reduce_max_sync(0xffffffffu, abits);
     if (NORM) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    if (lane_id() == 0) slot[warp_id()] = make_uint2(abits, __float_as_uint(ss));
-    __syncthreads();
-    const int warps = (int)(blockDim.x >> 5);
+    if (lane_id() == 0) slot[warp] = make_uint2(abits, __float_as_uint(ss));
+    named_bar_sync(1, (uint32_t)threads);
+    const int warps = threads >> 5;
     uint2 v = make_uint2(0u, 0u);
     if ((int)lane_id() < warps) v = slot[lane_id()];
     abits = __reduce_max_sync(0xffffffffu, v.x);
@@ -201,6 +215,27 @@ __device__ __forceinline__ uint32_t amax_bits8(const float (&t)[8], uint32_t m) 
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(t[i]) & 0x7FFFFFFFu);
     return m;
+}
+
+// Eight columns (vector c) of a row's outputs that need its factors.
+template <int T, bool NORM>
+__device__ __forceinline__ void store_row8(const QuantRowsArgs& a, int row, int c, const float (&h)[8],
+                                           const float (&gain)[8], const RowFactors& f) {
+    if (!NORM || a.codes) {
+        float t[8];
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) fmul2_rn(h[i], h[i + 1], gain[i], gain[i + 1], t[i], t[i + 1]);
+        uint2 code = codes8(t, f.inv);
+        if (f.inv == 0.0f) code = make_uint2(0u, 0u);   // also where t is not finite
+        *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.K + 8 * (int64_t)c) = code;
+    }
+    if (NORM && a.normed) {
+        float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+        if (a.norm_weight) raw_to_f32<T>(ld_raw8<T>(a.norm_weight, 8 * (int64_t)c), w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = __fmul_rn(__fmul_rn(h[i], f.rstd), w[i]);
+        st_f32x8<T>(a.normed, (int64_t)row * a.K + 8 * (int64_t)c, w);
+    }
 }
 
 // Rows held in registers: thread i of a block of T threads owns columns
@@ -273,33 +308,146 @@ __global__ void __launch_bounds__(q8::kMaxThreads) quantize_rows_w8_kernel(Quant
         }
         const int next = next_row(row, a.M);
         if (next < a.M) load_row(next);
-        block_reduce<NORM>(abits, ss, slots[buf]);
+        group_reduce<NORM>(abits, ss, slots[buf], (int)warp_id(), step);
+        const RowFactors f = row_factors<NORM>(abits, ss, a.K, a.eps);
+        if (a.scales && tid == 0) a.scales[row] = f.scale;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = tid + v * step;
+            if (c < nvec) store_row8<T, NORM>(a, row, c, h[v], gain[v], f);
+        }
+        row = next;
+    }
+}
+
+// The same rows streamed: thread 0 copies whole rows (x, and the residual
+// behind it) into a ring of shared memory, so that the bytes in flight are the
+// ring's and not what the registers of the threads can hold.  The barrier of a
+// row's reduction also says that every thread has read the row, so the copy
+// of a later row into its place follows it without a barrier of its own.
+namespace q8 {
+constexpr int kRingThreads = 1024;
+constexpr int kRingVec = 2;          // vectors of eight columns per thread (one: the same time; four: 96 registers)
+constexpr int kMaxRing = 8;
+constexpr int kRingBarBytes = 128;
+}  // namespace q8
+enum : uint32_t { kSiteQ8Full = 50, kSiteQ8Drain = 51 };
+
+template <int T>
+__device__ __forceinline__ Raw8<T> lds_raw8(const uint8_t* row, int vec) {
+    Raw8<T> r;
+    const uint4* p = reinterpret_cast<const uint4*>(row + (int64_t)vec * (T == kF32 ? 32 : 16));
+    r.w[0] = p[0];
+    if (T == kF32) r.w[T == kF32 ? 1 : 0] = p[1];
+    return r;
+}
+
+template <int T, bool NORM>
+__global__ void __launch_bounds__(q8::kRingThreads) quantize_rows_w8_ring_kernel(QuantRowsArgs a, int stages) {
+    using namespace q8;
+    constexpr int V = kRingVec;
+    extern __shared__ __align__(128) uint8_t ring[];   // barriers, then `stages` rows (x, residual)
+    __shared__ uint2 slots[2][32];
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring);
+    uint8_t* rows = ring + kRingBarBytes;
+    const int tid = (int)threadIdx.x, step = (int)blockDim.x;
+    const int nvec = a.K >> 3;
+    const bool has_res = NORM && a.residual != nullptr;
+    const uint32_t row_bytes = (uint32_t)a.K * (T == kF32 ? 4u : 2u);
+    const uint32_t stage_bytes = has_res ? 2u * row_bytes : row_bytes;
+    if (tid == 0) {
+        for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    // the previous kernel of the stream wrote what is read here
+    griddep_wait();
+    griddep_launch_dependents();
+    const auto fetch = [&](int row, int s) {   // thread 0
+        constexpr int b = T == kF32 ? 4 : 2;
+        uint8_t* dst = rows + (size_t)s * stage_bytes;
+        mbar_arrive_expect_tx(&full[s], stage_bytes);
+        bulk_load(dst, reinterpret_cast<const uint8_t*>(a.x) + (int64_t)row * a.ldx * b, row_bytes, &full[s]);
+        if (has_res)
+            bulk_load(dst + row_bytes, reinterpret_cast<const uint8_t*>(a.residual) + (int64_t)row * a.ldr * b,
+                      row_bytes, &full[s]);
+    };
+    int ahead = (int)blockIdx.x;   // thread 0: the next row to fetch
+    if (tid == 0)
+        for (int s = 0; s < stages && ahead < a.M; ++s, ahead = next_row(ahead, a.M)) fetch(ahead, s);
+    float gain[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int c = tid + v * step;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gain[v][i] = 1.0f;
+        if (c < nvec) {
+            if (NORM && a.norm_weight) raw_to_f32<T>(ld_raw8<T>(a.norm_weight, 8 * (int64_t)c), gain[v]);
+            if (a.gain) {
+                float g[8];
+                raw_to_f32<kF32>(ld_raw8<kF32>(a.gain, 8 * (int64_t)c), g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) gain[v][i] = __fmul_rn(gain[v][i], g[i]);
+            }
+        }
+    }
+    int s = 0, buf = 0;
+    uint32_t ph = 0u;
+    bool alive = true;
+    for (int row = (int)blockIdx.x; row < a.M; row = next_row(row, a.M), buf ^= 1) {
+        // after a timeout the block runs on without waiting and without fetching (its rows are void)
+        if (alive) alive = bounded_wait(&full[s], ph, kSiteQ8Full);
+        const uint8_t* src = rows + (size_t)s * stage_bytes;
+        float h[V][8];
+        uint32_t abits = 0u;
+        float ss = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int c = tid + v * step;
+            if (c < nvec) {
+                raw_to_f32<T>(lds_raw8<T>(src, c), h[v]);
+                if (has_res) {
+                    float r[8];
+                    raw_to_f32<T>(lds_raw8<T>(src + row_bytes, c), r);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2)
+                        fadd2_rn(h[v][i], h[v][i + 1], r[i], r[i + 1], h[v][i], h[v][i + 1]);
+                }
+                float t[8];
+#pragma unroll
+                for (int i = 0; i < 8; i += 2)
+                    fmul2_rn(h[v][i], h[v][i + 1], gain[v][i], gain[v][i + 1], t[i], t[i + 1]);
+                abits = amax_bits8(t, abits);
+                if (NORM) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
+                }
+            }
+        }
+        group_reduce<NORM>(abits, ss, slots[buf], (int)warp_id(), step);
+        if (tid == 0 && alive && ahead < a.M) {
+            fetch(ahead, s);
+            ahead = next_row(ahead, a.M);
+        }
+        if (++s == stages) {
+            s = 0;
+            ph ^= 1u;
+        }
         const RowFactors f = row_factors<NORM>(abits, ss, a.K, a.eps);
         if (a.scales && tid == 0) a.scales[row] = f.scale;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = tid + v * step;
             if (c < nvec) {
-                if (!NORM || a.codes) {
-                    float t[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2)
-                        fmul2_rn(h[v][i], h[v][i + 1], gain[v][i], gain[v][i + 1], t[i], t[i + 1]);
-                    uint2 code = codes8(t, f.inv);
-                    if (f.inv == 0.0f) code = make_uint2(0u, 0u);   // also where t is not finite
-                    *reinterpret_cast<uint2*>(a.codes + (int64_t)row * a.K + 8 * c) = code;
-                }
-                if (NORM && a.normed) {
-                    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-                    if (a.norm_weight) raw_to_f32<T>(ld_raw8<T>(a.norm_weight, 8 * (int64_t)c), w);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = __fmul_rn(__fmul_rn(h[v][i], f.rstd), w[i]);
-                    st_f32x8<T>(a.normed, (int64_t)row * a.K + 8 * c, w);
-                }
+                if (NORM && a.h_out) st_f32x8<T>(a.h_out, (int64_t)row * a.K + 8 * c, h[v]);
+                store_row8<T, NORM>(a, row, c, h[v], gain[v], f);
             }
         }
-        row = next;
     }
+    // no copy is in flight when the block ends, even after a timeout: the
+    // stages from s on were fetched and not waited for (best effort, bounded)
+    if (tid == 0 && !alive)
+        for (int i = 0; i < stages; ++i) mbar_wait(&full[i], 0u, kSiteQ8Drain);
 }
 
 // Rows too wide for the registers of one block: statistics in a first pass
@@ -349,7 +497,7 @@ __global__ void __launch_bounds__(q8::kTwoPassThreads) quantize_rows_w8_wide_ker
             }
             abits = amax_bits8(t, abits);
         }
-        block_reduce<NORM>(abits, ss, slots[buf]);
+        group_reduce<NORM>(abits, ss, slots[buf], (int)warp_id(), step);
         const RowFactors f = row_factors<NORM>(abits, ss, a.K, a.eps);
         if (a.scales && tid == 0) a.scales[row] = f.scale;
 #pragma unroll 2

@@ -97,6 +97,14 @@ svdq_status launch_status(const char* where) {
     return SVDQ_ERR_CUDA;
 }
 
+template <int NT>
+bool set_narrow_limits() {
+    const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    return cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kBf16>, attr, kNarrowSmemBudget) == cudaSuccess &&
+           cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kF16>, attr, kNarrowSmemBudget) == cudaSuccess &&
+           cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kF32>, attr, kNarrowSmemBudget) == cudaSuccess;
+}
+
 // Rejects anything but compute capability 10.0 before any launch, and sets
 // the kernels' shared-memory limits once per device.
 svdq_status check_device() {
@@ -143,14 +151,8 @@ svdq_status check_device() {
                                  (int)w8p::SMEM_BYTES) != cudaSuccess ||
             cudaFuncSetAttribute(gemm_w8a8_pair_kernel<kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)w8p::SMEM_BYTES) != cudaSuccess ||
-            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kNarrowSmemBudget) != cudaSuccess ||
-            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kNarrowSmemBudget) != cudaSuccess ||
-            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kNarrowSmemBudget) != cudaSuccess ||
-            cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kNarrowSmemBudget) != cudaSuccess)
+            !set_narrow_limits<16>() || !set_narrow_limits<32>() || !set_narrow_limits<64>() ||
+            !set_narrow_limits<128>())
             return cuda_fail("setting kernel shared-memory limits");
         g_device_ready[dev] = true;
     }
@@ -231,6 +233,16 @@ bool make_sf_map(CUtensorMap* m, const void* base, uint64_t row_blocks, uint64_t
         snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled (scale blocks) failed (CUresult %d)",
                  (int)r);
     return r == CUDA_SUCCESS;
+}
+
+// The current device, which check_device has found to be one of the first kMaxDevices.
+int current_device() {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        dev = 0;
+    }
+    return dev;
 }
 
 // SM count of the current device (looked up once per device).
@@ -777,18 +789,14 @@ bool overlaps(const void* p, int64_t np, const void* q, int64_t nq) {
     return p != nullptr && q != nullptr && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
 }
 
-// Blocks of `threads` threads that one SM holds, looked up once per device.
+// Blocks of `threads` threads and `smem` bytes of dynamic shared memory that one SM holds (`slot`: looked up
+// once per device and block size).
+constexpr int kRowThreads = 33;
 template <typename Kernel>
-int blocks_per_sm(Kernel kernel, int threads, std::atomic<int>* cache) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
-        cudaGetLastError();
-        return 1;
-    }
-    std::atomic<int>& slot = cache[dev * 33 + threads / 32];
+int blocks_per_sm(Kernel kernel, int threads, size_t smem, std::atomic<int>& slot) {
     int n = slot.load();
     if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) {
             cudaGetLastError();
             n = 1;
         }
@@ -797,30 +805,74 @@ int blocks_per_sm(Kernel kernel, int threads, std::atomic<int>* cache) {
     return n;
 }
 
-template <typename Kernel>
-svdq_status launch_rows(Kernel kernel, int threads, std::atomic<int>* cache, const QuantRowsArgs& a, cudaStream_t st) {
-    const int64_t grid = std::min<int64_t>(a.M, (int64_t)num_sms() * blocks_per_sm(kernel, threads, cache));
-    if (launch_ex(kernel, dim3((unsigned)grid), dim3((unsigned)threads), 0, st, 1u, a) != cudaSuccess)
-        return cuda_fail("quantize_rows_w8_kernel launch");
-    return launch_status("quantize_rows_w8_kernel launch");
+template <typename Kernel, typename... Args>
+svdq_status launch_rows(Kernel kernel, int threads, size_t smem, int blocks, const QuantRowsArgs& a, cudaStream_t st,
+                        Args... args) {
+    const int64_t grid = std::min<int64_t>(a.M, (int64_t)num_sms() * blocks);
+    if (launch_ex(kernel, dim3((unsigned)grid), dim3((unsigned)threads), smem, st, 1u, a, args...) != cudaSuccess)
+        return cuda_fail("W8A8 row quantizer launch");
+    return launch_status("W8A8 row quantizer launch");
 }
 
 template <int T, bool NORM, int V>
 svdq_status quantize_rows_held(const QuantRowsArgs& a, cudaStream_t st) {
-    static std::atomic<int> cache[kMaxDevices * 33];
+    static std::atomic<int> cache[kMaxDevices][kRowThreads];
     const int threads = (int)round_up((a.K / 8 + V - 1) / V, 32);
-    return launch_rows(quantize_rows_w8_kernel<T, NORM, V>, threads, cache, a, st);
+    const auto kernel = quantize_rows_w8_kernel<T, NORM, V>;
+    const int dev = current_device();
+    return launch_rows(kernel, threads, 0, blocks_per_sm(kernel, threads, 0, cache[dev][threads / 32]), a, st);
 }
 
+// Of a block's share of an SM's shared memory, what is not rows: barriers, statics, the system's 1 KB.
+constexpr int kRingSlack = 2048;
+template <int T, bool NORM>
+svdq_status quantize_rows_ring(const QuantRowsArgs& a, int blocks, cudaStream_t st) {
+    const auto kernel = quantize_rows_w8_ring_kernel<T, NORM>;
+    const int dev = current_device();
+    static std::atomic<bool> ready[kMaxDevices];
+    if (!ready[dev].load()) {
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmemBudget) !=
+            cudaSuccess)
+            return cuda_fail("setting the W8A8 row quantizer's shared memory");
+        ready[dev].store(true);
+    }
+    const int threads = (int)round_up((a.K / 8 + q8::kRingVec - 1) / q8::kRingVec, 32);
+    const int64_t stage = (int64_t)a.K * (T == kF32 ? 4 : 2) * (a.residual ? 2 : 1);
+    const int64_t stages = std::min<int64_t>((kNarrowSmemBudget / blocks - kRingSlack) / stage, q8::kMaxRing);
+    if (stages < 2) return SVDQ_ERR_UNSUPPORTED_SHAPE;   // the caller's choice of blocks leaves room for two
+    const size_t smem = q8::kRingBarBytes + (size_t)(stages * stage);
+    // the blocks that are resident at once share the rows (registers may allow fewer than asked for)
+    static std::atomic<int> cache[kMaxDevices][kRowThreads];
+    const int fit = blocks_per_sm(kernel, threads, 0, cache[dev][threads / 32]);
+    return launch_rows(kernel, threads, smem, std::min(blocks, fit), a, st, (int)stages);
+}
+
+// Which kernel quantises rows of a width (measured on bf16 rows from HBM; us):
+//   * the ring where a row's bytes (x and residual) reach 16 KB and two rows
+//     fit: norm, M = 4608: K = 4096 24.2 (held 25.7), K = 2048 14.1 (13.9);
+//     norm, M = 16384, K = 8192 160 (held 223); quantise, M = 4608, K = 12288
+//     35.0 (42.6), K = 4096 13.2 (12.6).  Two blocks per SM when they can each
+//     hold two rows, but one, with all the memory, for rows of 32 KB in large
+//     numbers (M = 16384, K = 8192: 160 against 170; M = 600: 11.0 against 9.4).
+//   * else in registers: one vector of eight per thread with a norm (M = 4608,
+//     K = 2048: 13.9, two vectors 15.1), two without (8.6 and 7.2);
+//   * else in two passes.
 template <int T, bool NORM>
 svdq_status quantize_rows_typed(const QuantRowsArgs& a, cudaStream_t st) {
     const int nvec = a.K / 8;
-    constexpr int kMaxV = T == kF32 && NORM ? 2 : 4;   // what fits in registers without spilling
-    if (nvec <= 256) return quantize_rows_held<T, NORM, 1>(a, st);
-    if (nvec <= 1024) return quantize_rows_held<T, NORM, 2>(a, st);
-    if (nvec <= kMaxV * q8::kMaxThreads) return quantize_rows_held<T, NORM, kMaxV>(a, st);
-    static std::atomic<int> cache[kMaxDevices * 33];
-    return launch_rows(quantize_rows_w8_wide_kernel<T, NORM>, q8::kTwoPassThreads, cache, a, st);
+    const int64_t stage = (int64_t)a.K * (T == kF32 ? 4 : 2) * (a.residual ? 2 : 1);
+    if (stage >= 16384 && nvec <= 2 * q8::kRingThreads && 2 * stage + kRingSlack <= kNarrowSmemBudget) {
+        int blocks = nvec <= 512 ? 4 : 2;
+        while (blocks > 1 && 2 * stage + kRingSlack > kNarrowSmemBudget / blocks) blocks /= 2;
+        if (stage >= 32768 && a.M >= 16 * num_sms()) blocks = 1;
+        return quantize_rows_ring<T, NORM>(a, blocks, st);
+    }
+    if (nvec <= (NORM ? q8::kMaxThreads : 128)) return quantize_rows_held<T, NORM, 1>(a, st);
+    if (nvec <= 2 * q8::kMaxThreads) return quantize_rows_held<T, NORM, 2>(a, st);
+    static std::atomic<int> cache[kMaxDevices];
+    const auto kernel = quantize_rows_w8_wide_kernel<T, NORM>;
+    return launch_rows(kernel, q8::kTwoPassThreads, 0,
+                       blocks_per_sm(kernel, q8::kTwoPassThreads, 0, cache[current_device()]), a, st);
 }
 
 template <bool NORM>
@@ -835,36 +887,74 @@ struct W8Plan {
     bool pair;
     int nt, split, stages;   // narrow kernel: tokens of a tile, CTAs sharing its K range, ring depth
 };
+// Stages of the narrow kernel's ring: as many as shared memory holds, one when
+// a CTA has no more to do, else an even number, so that each place in the ring
+// belongs to one of the two MMA warps (a warp must see every phase of a
+// barrier that it waits on: parities repeat).
+int w8_ring(int nt, int split, int64_t chunks) {
+    const int64_t most = ((chunks + split - 1) / split + w8n::per(nt) - 1) / w8n::per(nt);
+    const int64_t room = (kNarrowSmemBudget - w8n::fixed_bytes(nt, split)) / w8n::stage_bytes(nt);
+    if (most == 1) return 1;
+    return (int)(std::min<int64_t>({(int64_t)w8n::kMaxStages, room, most + 1}) / 2 * 2);
+}
+// The kernel and tile whose estimated time is least, in nanoseconds:
+//   pair:   5950 + load(waves x 290 per chunk of 128 bytes of K)
+//   narrow: 2650 + load(waves x chunks of a CTA x t) + (split: 1050 + 96 per token that a CTA finishes)
+// with t = 150, 150, 224, 316 for tiles of 16, 32, 64, 128 tokens and load(x) =
+// the larger of x and the weight's time from HBM (5.7 TB/s) plus a quarter of
+// the smaller.  The constants are fitted to 500 timings at 74 shapes (1 to 2200
+// tokens, N 1024 to 28672, K 1024 to 13824, weights from HBM): the choice is
+// on average 0.1 % slower than the best candidate, at most 9 %.  Examples of
+// both sides: 256 tokens, N = K = 4096: 64-token tiles 9.7 us, pairs 15.7;
+// 1000 tokens: 128-token tiles 24.6, pairs 16.9; one token, N = K = 4096:
+// split in four 6.5, not split 7.8.
 W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t chunks = (K + w8n::BK - 1) / w8n::BK;
-    const int64_t pair_tiles = ((M + w8p::BM - 1) / w8p::BM) * ((N + w8p::BN - 1) / w8p::BN);
-    const int mode = g_gemm_tiles_mode.load();
-    W8Plan p = {};
-    p.pair = mode == 2 || (mode == 0 && M > 128 && pair_tiles >= 40);
-    if (p.pair) return p;
-    p.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    const int64_t tiles = ((M + p.nt - 1) / p.nt) * ((N + w8n::BN - 1) / w8n::BN);
+    const int64_t weights_ns = N * K / 5700;
+    const auto load = [&](int64_t x) { return std::max(x, weights_ns) + std::min(x, weights_ns) / 4; };
     const int sms = num_sms();
-    p.split = 1;
-    while (p.split < w8n::kMaxSplit && tiles * p.split * 2 <= 2 * sms && chunks / (2 * p.split) >= 4) p.split *= 2;
-    const bool two = tiles * p.split > sms;   // two blocks per SM
-    const int budget = (two ? kNarrowSmemBudget / 2 : kNarrowSmemBudget) - w8n::fixed_bytes(p.nt);
-    const int64_t most = (chunks + p.split - 1) / p.split;
-    p.stages = (int)std::min<int64_t>({(int64_t)w8n::kMaxStages, (int64_t)(budget / w8n::stage_bytes(p.nt)), most});
-    // the partial sums need the room of the ring
-    const int need = (w8n::partial_bytes(p.nt) + w8n::stage_bytes(p.nt) - 1) / w8n::stage_bytes(p.nt);
-    if (p.split > 1) p.stages = std::max(p.stages, need);
-    return p;
+    const int mode = g_gemm_tiles_mode.load();
+    W8Plan best = {true, 0, 0, 0};
+    int64_t best_ns = INT64_MAX;
+    if (mode != 1) {
+        const int64_t tiles = ((M + w8p::BM - 1) / w8p::BM) * ((N + w8p::BN - 1) / w8p::BN);
+        const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
+        best_ns = 5950 + load(waves * chunks * 290);
+    }
+    if (mode == 2) return best;
+    constexpr int kNt[4] = {16, 32, 64, 128}, kChunkNs[4] = {150, 150, 224, 316};
+    // CTAs of a split that are resident at once: clusters of 4 and 8 leave SMs
+    // of a GPC unused (33 and 15 of them fit 148 SMs)
+    const int slots[4] = {sms, sms / 2 * 2, sms * 132 / 148, sms * 120 / 148};
+    for (int i = 0; i < 4; ++i) {
+        const int nt = kNt[i];
+        const int64_t mt = (M + nt - 1) / nt, ntl = (N + w8n::BN - 1) / w8n::BN;
+        if (mt > 65535 || ntl > 65535) continue;   // the grid's limits
+        for (int l = 0; l < 4 && (1 << l) <= chunks; ++l) {
+            const int64_t waves = (((mt * ntl) << l) + slots[l] - 1) / slots[l];
+            const int64_t of_cta = (chunks + (1 << l) - 1) >> l;
+            int64_t ns = 2650 + load(waves * of_cta * kChunkNs[i]);
+            if (l > 0) ns += 1050 + 96 * ((std::min<int64_t>(M, nt) + (1 << l) - 1) >> l);
+            if (ns < best_ns) {
+                best_ns = ns;
+                best = {false, nt, 1 << l, w8_ring(nt, 1 << l, chunks)};
+            }
+        }
+    }
+    return best;
 }
 
 template <int NT>
 svdq_status gemm_w8a8_narrow(const W8Plan& p, const CUtensorMap& tm_x, const CUtensorMap& tm_w, GemmW8Args a,
-                             cudaStream_t st) {
+                             svdq_dtype out, cudaStream_t st) {
     a.stages = p.stages;
-    const size_t smem = (size_t)w8n::fixed_bytes(NT) + (size_t)p.stages * w8n::stage_bytes(NT);
+    const size_t smem = (size_t)w8n::fixed_bytes(NT, p.split) + (size_t)p.stages * w8n::stage_bytes(NT);
+    if (p.stages < 1 || smem > (size_t)kNarrowSmemBudget) return SVDQ_ERR_UNSUPPORTED_SHAPE;   // no plan is so
     const dim3 grid((unsigned)p.split, (unsigned)a.n_tiles, (unsigned)a.m_tiles);
-    if (launch_ex(gemm_w8a8_narrow_kernel<NT>, grid, dim3(w8n::kThreads), smem, st, (unsigned)p.split, tm_x, tm_w,
-                  a) != cudaSuccess)
+    const auto kernel = out == SVDQ_F32   ? gemm_w8a8_narrow_kernel<NT, kF32>
+                        : out == SVDQ_F16 ? gemm_w8a8_narrow_kernel<NT, kF16>
+                                          : gemm_w8a8_narrow_kernel<NT, kBf16>;
+    if (launch_ex(kernel, grid, dim3(w8n::kThreads), smem, st, (unsigned)p.split, tm_x, tm_w, a) != cudaSuccess)
         return cuda_fail("gemm_w8a8_narrow_kernel launch");
     return launch_status("gemm_w8a8_narrow_kernel launch");
 }
@@ -882,7 +972,6 @@ svdq_status gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, con
     a.N = (int)N;
     a.chunks = (int)((K + 127) / 128);
     a.last_steps = (int)((K - 128 * (int64_t)(a.chunks - 1) + 31) / 32);
-    a.out = out;
     const int64_t tm = p.pair ? w8p::BM : p.nt, tn = p.pair ? w8p::BN : w8n::BN;
     const int64_t mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
     if (p.pair ? mt * nt > (int64_t(1) << 30) : (mt > 65535 || nt > 65535)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
@@ -894,10 +983,10 @@ svdq_status gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, con
         !make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128))
         return SVDQ_ERR_CUDA;
     if (!p.pair) {
-        if (p.nt == 16) return gemm_w8a8_narrow<16>(p, tm_x, tm_w, a, st);
-        if (p.nt == 32) return gemm_w8a8_narrow<32>(p, tm_x, tm_w, a, st);
-        if (p.nt == 64) return gemm_w8a8_narrow<64>(p, tm_x, tm_w, a, st);
-        return gemm_w8a8_narrow<128>(p, tm_x, tm_w, a, st);
+        if (p.nt == 16) return gemm_w8a8_narrow<16>(p, tm_x, tm_w, a, out, st);
+        if (p.nt == 32) return gemm_w8a8_narrow<32>(p, tm_x, tm_w, a, out, st);
+        if (p.nt == 64) return gemm_w8a8_narrow<64>(p, tm_x, tm_w, a, out, st);
+        return gemm_w8a8_narrow<128>(p, tm_x, tm_w, a, out, st);
     }
     // y leaves through TMA stores of boxes of 32 rows x 64 bytes
     CUtensorMap tm_y;

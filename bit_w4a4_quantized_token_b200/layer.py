@@ -145,90 +145,126 @@ class QuantizedActW8A8:
     x_scales: torch.Tensor              # fp32 [M]
 
 
-def _check_tensor(name: str, t: torch.Tensor, dtype, shape: tuple, device) -> None:
-    """What the library cannot see of a contiguous operand behind its pointer."""
-    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+# The small calls of this layer are bound by what the host does per call, so the current device and stream are
+# asked for without building torch.cuda's objects (3 us for current_stream alone), and the library is called with
+# plain addresses.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _check_tensor(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> None:
+    """What the library cannot see of a contiguous operand behind its pointer (index: the call's GPU)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {index}, got "
                          f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
 
 
 def _check_rows(name: str, x: torch.Tensor, K: int) -> int:
     """The library's type of a matrix of activations; rows may be apart, elements of a row not."""
-    if x.dim() != 2 or x.shape[1] != K or x.dtype not in _DTYPES or not x.is_cuda or (K > 1 and x.stride(1) != 1):
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None or x.dim() != 2 or x.shape[1] != K or not x.is_cuda or (x.stride(1) != 1 and K > 1):
         raise ValueError(f"{name}: expected a CUDA matrix [M, {K}] of bf16, fp16 or fp32 with contiguous rows, got "
                          f"{x.dtype} {tuple(x.shape)} (strides {x.stride()}) on {x.device}")
-    return _DTYPES[x.dtype]
+    return dtype
 
 
 def _row_stride(x: torch.Tensor) -> int:
     return x.stride(0) if x.shape[0] > 1 else x.shape[1]
 
 
-def _run_on(device, stream, fn, args: tuple, tensors: tuple) -> None:
-    """Calls the binding on `stream` (None: the current one) with `device` current.  The tensors of a call on
-    another stream are marked as in use there, so that the allocator does not hand out their memory early."""
-    if device.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got tensors on {device}")
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            _run_on(device, stream, fn, args, tensors)
-        return
-    current = torch.cuda.current_stream().cuda_stream
-    handle = current if stream is None else stream if isinstance(stream, int) else stream.cuda_stream
-    fn(*args, handle)
-    if handle != current:
-        used = torch.cuda.ExternalStream(handle, device=device)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(used)
+def _addr(t: torch.Tensor | None) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _call(name: str, index: int, args: tuple) -> None:
+    """Calls a library entry point on the current stream of GPU `index`."""
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return _call(name, index, args)
+    status = getattr(_lib.lib, name)(*args, _current_stream(index))
+    if status != _lib.SVDQ_OK:
+        raise _lib.SvdqError(status, name)
+
+
+def _tensors(v):
+    """The tensors of an argument or a result."""
+    if isinstance(v, torch.Tensor):
+        yield v
+    elif isinstance(v, (PackedWeightW8A8, QuantizedActW8A8)):
+        yield from _tensors(tuple(vars(v).values()))
+    elif isinstance(v, tuple):
+        for t in v:
+            yield from _tensors(t)
+
+
+def _on_stream(stream, x: torch.Tensor, fn, *args):
+    """fn(*args) with `stream` (a torch stream or a raw handle) current, so that what it allocates is ordered with
+    that stream's work.  The tensors it reads are marked as in use there, those it returns as in use on the caller's
+    stream, so that the allocator hands out no memory early; the two streams' order is the caller's to keep."""
+    caller = torch.cuda.current_stream(x.device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)
+    with torch.cuda.stream(stream):
+        result = fn(*args)
+    if stream != caller:
+        for t in _tensors(args):
+            t.record_stream(stream)
+        for t in _tensors(result):
+            t.record_stream(caller)
+    return result
 
 
 def pack_weight_w8a8(W: torch.Tensor, lam: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                      stream=None) -> PackedWeightW8A8:
     """W [N, K] bf16, fp16 or fp32 -> 8-bit codes and a scale per output channel.  With smoothing divisors
     lam [K] (fp32) the rows W * lam are quantised and activations are divided by lam."""
+    if stream is not None:
+        return _on_stream(stream, W, pack_weight_w8a8, W, lam, bias)
     N, K = W.shape
     w_type = _check_rows("W", W, K)
     W = W.contiguous()
-    dev = W.device
+    dev, index = W.device, W.get_device()
     if lam is not None:
-        _check_tensor("lam", lam, torch.float32, (K,), dev)
-    if bias is not None and (bias.shape != (N,) or bias.dtype not in _DTYPES or bias.device != dev):
+        _check_tensor("lam", lam, torch.float32, (K,), index)
+    if bias is not None and (bias.shape != (N,) or bias.dtype not in _DTYPES or bias.get_device() != index):
         raise ValueError(f"bias: expected a bf16, fp16 or fp32 tensor of shape ({N},) on {dev}, got {bias.dtype} "
                          f"{tuple(bias.shape)} on {bias.device}")
     w_codes = torch.empty(N, K, dtype=torch.int8, device=dev)
     w_scales = torch.empty(N, dtype=torch.float32, device=dev)
     inv_lambda = torch.empty(K, dtype=torch.float32, device=dev) if lam is not None else None
-    _run_on(dev, stream, _lib.svdq_pack_weight_w8a8, (w_type, W, N, K, lam, w_codes, w_scales, inv_lambda),
-            (W, lam, w_codes, w_scales, inv_lambda))
+    _call("svdq_pack_weight_w8a8", index,
+          (w_type, W.data_ptr(), N, K, _addr(lam), w_codes.data_ptr(), w_scales.data_ptr(), _addr(inv_lambda)))
     return PackedWeightW8A8(N, K, w_codes, w_scales, inv_lambda, None if bias is None else bias.contiguous())
 
 
 def alloc_act_w8a8(packed: PackedWeightW8A8, M: int, device) -> QuantizedActW8A8:
-    return QuantizedActW8A8(M, torch.empty(M, packed.K, dtype=torch.int8, device=device),
-                            torch.empty(M, dtype=torch.float32, device=device))
+    return QuantizedActW8A8(M, torch.empty((M, packed.K), dtype=torch.int8, device=device),
+                            torch.empty((M,), dtype=torch.float32, device=device))
 
 
-def _act_out(packed: PackedWeightW8A8, M: int, device, out: QuantizedActW8A8 | None) -> QuantizedActW8A8:
+def _act_out(packed: PackedWeightW8A8, M: int, x: torch.Tensor, index: int,
+             out: QuantizedActW8A8 | None) -> QuantizedActW8A8:
     if out is None:
-        return alloc_act_w8a8(packed, M, device)
-    _check_tensor("out.x_codes", out.x_codes, torch.int8, (M, packed.K), device)
-    _check_tensor("out.x_scales", out.x_scales, torch.float32, (M,), device)
+        return alloc_act_w8a8(packed, M, x.device)
+    _check_tensor("out.x_codes", out.x_codes, torch.int8, (M, packed.K), index)
+    _check_tensor("out.x_scales", out.x_scales, torch.float32, (M,), index)
     return out
 
 
 def quantize_act_w8a8(x: torch.Tensor, packed: PackedWeightW8A8, out: QuantizedActW8A8 | None = None,
                       stream=None) -> QuantizedActW8A8:
     """x [M, K] bf16, fp16 or fp32 (rows may be apart) -> 8-bit codes and a scale per token."""
-    M, K = x.shape[0], packed.K
+    if stream is not None:
+        return _on_stream(stream, x, quantize_act_w8a8, x, packed, out)
+    K, inv_lambda = packed.K, packed.inv_lambda
     x_type = _check_rows("x", x, K)
-    dev = x.device
-    if packed.inv_lambda is not None:
-        _check_tensor("packed.inv_lambda", packed.inv_lambda, torch.float32, (K,), dev)
-    q = _act_out(packed, M, dev, out)
-    _run_on(dev, stream, _lib.svdq_quantize_act_w8a8,
-            (x_type, x, _row_stride(x), M, K, packed.inv_lambda, q.x_codes, q.x_scales),
-            (x, packed.inv_lambda, q.x_codes, q.x_scales))
+    M, index = x.shape[0], x.get_device()
+    if inv_lambda is not None:
+        _check_tensor("packed.inv_lambda", inv_lambda, torch.float32, (K,), index)
+    q = _act_out(packed, M, x, index, out)
+    _call("svdq_quantize_act_w8a8", index,
+          (x_type, x.data_ptr(), _row_stride(x), M, K, _addr(inv_lambda), q.x_codes.data_ptr(),
+           q.x_scales.data_ptr()))
     return q
 
 
@@ -239,30 +275,32 @@ def rms_norm_quantize_w8a8(x: torch.Tensor, residual: torch.Tensor | None, norm_
     """h = x + residual, its RMSNorm, and the 8-bit codes of that: returns (h, codes and scales).  h goes to h_out
     (a new tensor by default; x or residual itself for an update in place); with residual None and no h_out, h is
     x.  The normalised rows are also written, in x's type, to `normed` when that is given."""
-    M, K = x.shape[0], packed.K
+    if stream is not None:
+        return _on_stream(stream, x, rms_norm_quantize_w8a8, x, residual, norm_weight, packed, eps, h_out, normed,
+                          out)
+    K, inv_lambda = packed.K, packed.inv_lambda
     x_type = _check_rows("x", x, K)
-    dev, dt = x.device, x.dtype
+    M, index, dt = x.shape[0], x.get_device(), x.dtype
     ldr = K
     if residual is not None:
-        if _check_rows("residual", residual, K) != x_type or residual.shape[0] != M or residual.device != dev:
-            raise ValueError(f"residual: expected {dt} {(M, K)} on {dev}, got {residual.dtype} "
+        if _check_rows("residual", residual, K) != x_type or residual.shape[0] != M or residual.get_device() != index:
+            raise ValueError(f"residual: expected {dt} {(M, K)} on {x.device}, got {residual.dtype} "
                              f"{tuple(residual.shape)} on {residual.device}")
         ldr = _row_stride(residual)
     if norm_weight is not None:
-        _check_tensor("norm_weight", norm_weight, dt, (K,), dev)
-    if packed.inv_lambda is not None:
-        _check_tensor("packed.inv_lambda", packed.inv_lambda, torch.float32, (K,), dev)
+        _check_tensor("norm_weight", norm_weight, dt, (K,), index)
+    if inv_lambda is not None:
+        _check_tensor("packed.inv_lambda", inv_lambda, torch.float32, (K,), index)
     if h_out is not None:
-        _check_tensor("h_out", h_out, dt, (M, K), dev)
+        _check_tensor("h_out", h_out, dt, (M, K), index)
     elif residual is not None:
-        h_out = torch.empty(M, K, dtype=dt, device=dev)
+        h_out = torch.empty((M, K), dtype=dt, device=x.device)
     if normed is not None:
-        _check_tensor("normed", normed, dt, (M, K), dev)
-    q = _act_out(packed, M, dev, out)
-    _run_on(dev, stream, _lib.svdq_rms_norm_quantize_w8a8,
-            (x_type, x, _row_stride(x), residual, ldr, M, K, norm_weight, eps, packed.inv_lambda, h_out, normed,
-             q.x_codes, q.x_scales),
-            (x, residual, norm_weight, packed.inv_lambda, h_out, normed, q.x_codes, q.x_scales))
+        _check_tensor("normed", normed, dt, (M, K), index)
+    q = _act_out(packed, M, x, index, out)
+    _call("svdq_rms_norm_quantize_w8a8", index,
+          (x_type, x.data_ptr(), _row_stride(x), _addr(residual), ldr, M, K, _addr(norm_weight), eps,
+           _addr(inv_lambda), _addr(h_out), _addr(normed), q.x_codes.data_ptr(), q.x_scales.data_ptr()))
     return (x if h_out is None else h_out), q
 
 
@@ -270,24 +308,31 @@ def gemm_w8a8(q: QuantizedActW8A8, packed: PackedWeightW8A8, y: torch.Tensor | N
               out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
     """y [M, N] = x_scales[m] w_scales[n] sum_k codes + bias, in out_dtype (default: y's type, else the bias's,
     else bf16); the bias has that type too."""
-    M, N, K, dev = q.M, packed.N, packed.K, q.x_codes.device
+    if stream is not None:
+        return _on_stream(stream, q.x_codes, gemm_w8a8, q, packed, y, out_dtype)
+    M, N, K, bias = q.M, packed.N, packed.K, packed.bias
     if out_dtype is None:
-        out_dtype = y.dtype if y is not None else packed.bias.dtype if packed.bias is not None else torch.bfloat16
-    if out_dtype not in _DTYPES:
+        out_dtype = y.dtype if y is not None else bias.dtype if bias is not None else torch.bfloat16
+    y_type = _DTYPES.get(out_dtype)
+    if y_type is None:
         raise ValueError(f"out_dtype: expected bf16, fp16 or fp32, got {out_dtype}")
-    _check_tensor("q.x_codes", q.x_codes, torch.int8, (M, K), dev)
-    _check_tensor("q.x_scales", q.x_scales, torch.float32, (M,), dev)
-    _check_tensor("packed.w_codes", packed.w_codes, torch.int8, (N, K), dev)
-    _check_tensor("packed.w_scales", packed.w_scales, torch.float32, (N,), dev)
-    if packed.bias is not None:
-        _check_tensor("packed.bias", packed.bias, out_dtype, (N,), dev)
+    x_codes, x_scales, w_codes, w_scales = q.x_codes, q.x_scales, packed.w_codes, packed.w_scales
+    index = x_codes.get_device()
+    _check_tensor("q.x_codes", x_codes, torch.int8, (M, K), index)
+    _check_tensor("q.x_scales", x_scales, torch.float32, (M,), index)
+    _check_tensor("packed.w_codes", w_codes, torch.int8, (N, K), index)
+    _check_tensor("packed.w_scales", w_scales, torch.float32, (N,), index)
+    if bias is not None:
+        _check_tensor("packed.bias", bias, out_dtype, (N,), index)
+    if y is not None:
+        _check_tensor("y", y, out_dtype, (M, N), index)
+    if index < 0:
+        raise ValueError(f"expected CUDA tensors, got tensors on {x_codes.device}")
     if y is None:
-        y = torch.empty(M, N, dtype=out_dtype, device=dev)
-    else:
-        _check_tensor("y", y, out_dtype, (M, N), dev)
-    _run_on(dev, stream, _lib.svdq_gemm_w8a8,
-            (q.x_codes, q.x_scales, M, packed.w_codes, packed.w_scales, N, K, packed.bias, _DTYPES[out_dtype], y),
-            (q.x_codes, q.x_scales, packed.w_codes, packed.w_scales, packed.bias, y))
+        y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
+    _call("svdq_gemm_w8a8", index,
+          (x_codes.data_ptr(), x_scales.data_ptr(), M, w_codes.data_ptr(), w_scales.data_ptr(), N, K, _addr(bias),
+           y_type, y.data_ptr()))
     return y
 
 
