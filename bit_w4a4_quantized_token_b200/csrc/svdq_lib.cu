@@ -854,6 +854,8 @@ svdq_status quantize_rows_ring(const QuantRowsArgs& a, int blocks, cudaStream_t 
 //     35.0 (42.6), K = 4096 13.2 (12.6).  Two blocks per SM when they can each
 //     hold two rows, but one, with all the memory, for rows of 32 KB in large
 //     numbers (M = 16384, K = 8192: 160 against 170; M = 600: 11.0 against 9.4).
+//     fp32 norms of up to 4096 columns stay in registers all the same (M =
+//     16384, K = 4096: 148 against 154; M = 512: 6.8 against 8.8).
 //   * else in registers: one vector of eight per thread with a norm (M = 4608,
 //     K = 2048: 13.9, two vectors 15.1), two without (8.6 and 7.2);
 //   * else in two passes.
@@ -861,7 +863,9 @@ template <int T, bool NORM>
 svdq_status quantize_rows_typed(const QuantRowsArgs& a, cudaStream_t st) {
     const int nvec = a.K / 8;
     const int64_t stage = (int64_t)a.K * (T == kF32 ? 4 : 2) * (a.residual ? 2 : 1);
-    if (stage >= 16384 && nvec <= 2 * q8::kRingThreads && 2 * stage + kRingSlack <= kNarrowSmemBudget) {
+    const bool held_f32 = T == kF32 && NORM && nvec <= q8::kMaxThreads;
+    if (stage >= 16384 && !held_f32 && nvec <= 2 * q8::kRingThreads &&
+        2 * stage + kRingSlack <= kNarrowSmemBudget) {
         int blocks = nvec <= 512 ? 4 : 2;
         while (blocks > 1 && 2 * stage + kRingSlack > kNarrowSmemBudget / blocks) blocks /= 2;
         if (stage >= 32768 && a.M >= 16 * num_sms()) blocks = 1;

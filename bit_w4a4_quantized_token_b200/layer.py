@@ -14,7 +14,7 @@ The 8-bit integer (W8A8) layer, for the layers that 4 bits cost too much:
 """
 from __future__ import annotations
 
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import torch
 
@@ -128,7 +128,10 @@ def svdq_linear(x: torch.Tensor, packed: PackedWeight, x_tensor_scale=None, stre
 _DTYPES = {torch.bfloat16: _lib.SVDQ_BF16, torch.float16: _lib.SVDQ_F16, torch.float32: _lib.SVDQ_F32}
 
 
-@dataclass
+_I8, _F32 = torch.int8, torch.float32
+
+
+@dataclass(slots=True)
 class PackedWeightW8A8:
     N: int
     K: int
@@ -138,52 +141,58 @@ class PackedWeightW8A8:
     bias: torch.Tensor | None           # [N], of the output's type
 
 
-@dataclass
+@dataclass(slots=True)
 class QuantizedActW8A8:
     M: int
     x_codes: torch.Tensor               # int8 [M, K]
     x_scales: torch.Tensor              # fp32 [M]
 
 
-# The small calls of this layer are bound by what the host does per call, so the current device and stream are
-# asked for without building torch.cuda's objects (3 us for current_stream alone), and the library is called with
-# plain addresses.
+# A call of this layer on few tokens is bound by what the host does for it, so these functions ask torch for the
+# current device and stream without building torch.cuda's objects (3 us for current_stream alone), allocate with the
+# allocator's short form where torch has it (0.7 us a tensor, torch.empty 2.3), test operands in one expression each
+# and put the message together only for a refusal, and call the library with plain addresses.
 _current_device = torch._C._cuda_getDevice
 _current_stream = torch._C._cuda_getCurrentRawStream
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda as _empty_strided   # (sizes, strides, dtype)
+except ImportError:
+    def _empty_strided(size, stride, dtype):
+        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
 
 
-def _check_tensor(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> None:
-    """What the library cannot see of a contiguous operand behind its pointer (index: the call's GPU)."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {index}, got "
-                         f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+def _unfit(t: torch.Tensor, dtype, shape: tuple, index: int) -> bool:
+    """Whether a contiguous operand is not what the library will take it for behind its pointer."""
+    return t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous()
 
 
-def _check_rows(name: str, x: torch.Tensor, K: int) -> int:
-    """The library's type of a matrix of activations; rows may be apart, elements of a row not."""
-    dtype = _DTYPES.get(x.dtype)
-    if dtype is None or x.dim() != 2 or x.shape[1] != K or not x.is_cuda or (x.stride(1) != 1 and K > 1):
+def _refuse(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> None:
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {index}, got "
+                     f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
+
+
+def _rows(name: str, x: torch.Tensor, K: int) -> tuple[int, int, int]:
+    """(library's type, rows, row stride) of a matrix of activations; rows may be apart, elements of a row not."""
+    x_type, shape, strides = _DTYPES.get(x.dtype), x.shape, x.stride()
+    if x_type is None or len(shape) != 2 or shape[1] != K or strides[1] != 1 or not x.is_cuda:
         raise ValueError(f"{name}: expected a CUDA matrix [M, {K}] of bf16, fp16 or fp32 with contiguous rows, got "
-                         f"{x.dtype} {tuple(x.shape)} (strides {x.stride()}) on {x.device}")
-    return dtype
-
-
-def _row_stride(x: torch.Tensor) -> int:
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1]
+                         f"{x.dtype} {tuple(shape)} (strides {strides}) on {x.device}")
+    return x_type, shape[0], (strides[0] if shape[0] > 1 else K)
 
 
 def _addr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _call(name: str, index: int, args: tuple) -> None:
-    """Calls a library entry point on the current stream of GPU `index`."""
-    if _current_device() != index:
-        with torch.cuda.device(index):
-            return _call(name, index, args)
-    status = getattr(_lib.lib, name)(*args, _current_stream(index))
-    if status != _lib.SVDQ_OK:
+def _check(status: int, name: str) -> None:
+    if status:
         raise _lib.SvdqError(status, name)
+
+
+def _on_device(index: int, fn, *args):
+    """fn(*args) with GPU `index` current: where the operands are is where everything happens."""
+    with torch.cuda.device(index):
+        return fn(*args)
 
 
 def _tensors(v):
@@ -191,7 +200,7 @@ def _tensors(v):
     if isinstance(v, torch.Tensor):
         yield v
     elif isinstance(v, (PackedWeightW8A8, QuantizedActW8A8)):
-        yield from _tensors(tuple(vars(v).values()))
+        yield from _tensors(tuple(getattr(v, f.name) for f in fields(v)))
     elif isinstance(v, tuple):
         for t in v:
             yield from _tensors(t)
@@ -221,34 +230,40 @@ def pack_weight_w8a8(W: torch.Tensor, lam: torch.Tensor | None = None, bias: tor
     if stream is not None:
         return _on_stream(stream, W, pack_weight_w8a8, W, lam, bias)
     N, K = W.shape
-    w_type = _check_rows("W", W, K)
+    w_type = _rows("W", W, K)[0]
     W = W.contiguous()
     dev, index = W.device, W.get_device()
-    if lam is not None:
-        _check_tensor("lam", lam, torch.float32, (K,), index)
+    if lam is not None and _unfit(lam, _F32, (K,), index):
+        _refuse("lam", lam, _F32, (K,), index)
     if bias is not None and (bias.shape != (N,) or bias.dtype not in _DTYPES or bias.get_device() != index):
         raise ValueError(f"bias: expected a bf16, fp16 or fp32 tensor of shape ({N},) on {dev}, got {bias.dtype} "
                          f"{tuple(bias.shape)} on {bias.device}")
-    w_codes = torch.empty(N, K, dtype=torch.int8, device=dev)
-    w_scales = torch.empty(N, dtype=torch.float32, device=dev)
-    inv_lambda = torch.empty(K, dtype=torch.float32, device=dev) if lam is not None else None
-    _call("svdq_pack_weight_w8a8", index,
-          (w_type, W.data_ptr(), N, K, _addr(lam), w_codes.data_ptr(), w_scales.data_ptr(), _addr(inv_lambda)))
+    if index != _current_device():
+        return _on_device(index, pack_weight_w8a8, W, lam, bias)
+    w_codes = torch.empty(N, K, dtype=_I8, device=dev)
+    w_scales = torch.empty(N, dtype=_F32, device=dev)
+    inv_lambda = torch.empty(K, dtype=_F32, device=dev) if lam is not None else None
+    _check(_lib.lib.svdq_pack_weight_w8a8(w_type, W.data_ptr(), N, K, _addr(lam), w_codes.data_ptr(),
+                                          w_scales.data_ptr(), _addr(inv_lambda), _current_stream(index)),
+           "svdq_pack_weight_w8a8")
     return PackedWeightW8A8(N, K, w_codes, w_scales, inv_lambda, None if bias is None else bias.contiguous())
 
 
 def alloc_act_w8a8(packed: PackedWeightW8A8, M: int, device) -> QuantizedActW8A8:
-    return QuantizedActW8A8(M, torch.empty((M, packed.K), dtype=torch.int8, device=device),
-                            torch.empty((M,), dtype=torch.float32, device=device))
+    return QuantizedActW8A8(M, torch.empty(M, packed.K, dtype=_I8, device=device),
+                            torch.empty(M, dtype=_F32, device=device))
 
 
-def _act_out(packed: PackedWeightW8A8, M: int, x: torch.Tensor, index: int,
-             out: QuantizedActW8A8 | None) -> QuantizedActW8A8:
-    if out is None:
-        return alloc_act_w8a8(packed, M, x.device)
-    _check_tensor("out.x_codes", out.x_codes, torch.int8, (M, packed.K), index)
-    _check_tensor("out.x_scales", out.x_scales, torch.float32, (M,), index)
-    return out
+def _act(M: int, K: int) -> QuantizedActW8A8:
+    """alloc_act_w8a8 on the current GPU."""
+    return QuantizedActW8A8(M, _empty_strided((M, K), (K, 1), _I8), _empty_strided((M,), (1,), _F32))
+
+
+def _check_out(out: QuantizedActW8A8, M: int, K: int, index: int) -> None:
+    if _unfit(out.x_codes, _I8, (M, K), index):
+        _refuse("out.x_codes", out.x_codes, _I8, (M, K), index)
+    if _unfit(out.x_scales, _F32, (M,), index):
+        _refuse("out.x_scales", out.x_scales, _F32, (M,), index)
 
 
 def quantize_act_w8a8(x: torch.Tensor, packed: PackedWeightW8A8, out: QuantizedActW8A8 | None = None,
@@ -257,15 +272,19 @@ def quantize_act_w8a8(x: torch.Tensor, packed: PackedWeightW8A8, out: QuantizedA
     if stream is not None:
         return _on_stream(stream, x, quantize_act_w8a8, x, packed, out)
     K, inv_lambda = packed.K, packed.inv_lambda
-    x_type = _check_rows("x", x, K)
-    M, index = x.shape[0], x.get_device()
-    if inv_lambda is not None:
-        _check_tensor("packed.inv_lambda", inv_lambda, torch.float32, (K,), index)
-    q = _act_out(packed, M, x, index, out)
-    _call("svdq_quantize_act_w8a8", index,
-          (x_type, x.data_ptr(), _row_stride(x), M, K, _addr(inv_lambda), q.x_codes.data_ptr(),
-           q.x_scales.data_ptr()))
-    return q
+    x_type, M, ldx = _rows("x", x, K)
+    index = x.get_device()
+    if index != _current_device():
+        return _on_device(index, quantize_act_w8a8, x, packed, out)
+    if inv_lambda is not None and _unfit(inv_lambda, _F32, (K,), index):
+        _refuse("packed.inv_lambda", inv_lambda, _F32, (K,), index)
+    if out is None:
+        out = _act(M, K)
+    else:
+        _check_out(out, M, K, index)
+    _check(_lib.lib.svdq_quantize_act_w8a8(x_type, x.data_ptr(), ldx, M, K, _addr(inv_lambda), out.x_codes.data_ptr(),
+                                           out.x_scales.data_ptr(), _current_stream(index)), "svdq_quantize_act_w8a8")
+    return out
 
 
 def rms_norm_quantize_w8a8(x: torch.Tensor, residual: torch.Tensor | None, norm_weight: torch.Tensor | None,
@@ -279,29 +298,37 @@ def rms_norm_quantize_w8a8(x: torch.Tensor, residual: torch.Tensor | None, norm_
         return _on_stream(stream, x, rms_norm_quantize_w8a8, x, residual, norm_weight, packed, eps, h_out, normed,
                           out)
     K, inv_lambda = packed.K, packed.inv_lambda
-    x_type = _check_rows("x", x, K)
-    M, index, dt = x.shape[0], x.get_device(), x.dtype
-    ldr = K
+    x_type, M, ldx = _rows("x", x, K)
+    index, dt = x.get_device(), x.dtype
+    if index != _current_device():
+        return _on_device(index, rms_norm_quantize_w8a8, x, residual, norm_weight, packed, eps, h_out, normed, out)
+    ldr, r_addr = K, None
     if residual is not None:
-        if _check_rows("residual", residual, K) != x_type or residual.shape[0] != M or residual.get_device() != index:
+        r_type, r_rows, ldr = _rows("residual", residual, K)
+        if r_type != x_type or r_rows != M or residual.get_device() != index:
             raise ValueError(f"residual: expected {dt} {(M, K)} on {x.device}, got {residual.dtype} "
                              f"{tuple(residual.shape)} on {residual.device}")
-        ldr = _row_stride(residual)
-    if norm_weight is not None:
-        _check_tensor("norm_weight", norm_weight, dt, (K,), index)
-    if inv_lambda is not None:
-        _check_tensor("packed.inv_lambda", inv_lambda, torch.float32, (K,), index)
+        r_addr = residual.data_ptr()
+    if norm_weight is not None and _unfit(norm_weight, dt, (K,), index):
+        _refuse("norm_weight", norm_weight, dt, (K,), index)
+    if inv_lambda is not None and _unfit(inv_lambda, _F32, (K,), index):
+        _refuse("packed.inv_lambda", inv_lambda, _F32, (K,), index)
     if h_out is not None:
-        _check_tensor("h_out", h_out, dt, (M, K), index)
+        if _unfit(h_out, dt, (M, K), index):
+            _refuse("h_out", h_out, dt, (M, K), index)
     elif residual is not None:
-        h_out = torch.empty((M, K), dtype=dt, device=x.device)
-    if normed is not None:
-        _check_tensor("normed", normed, dt, (M, K), index)
-    q = _act_out(packed, M, x, index, out)
-    _call("svdq_rms_norm_quantize_w8a8", index,
-          (x_type, x.data_ptr(), _row_stride(x), _addr(residual), ldr, M, K, _addr(norm_weight), eps,
-           _addr(inv_lambda), _addr(h_out), _addr(normed), q.x_codes.data_ptr(), q.x_scales.data_ptr()))
-    return (x if h_out is None else h_out), q
+        h_out = _empty_strided((M, K), (K, 1), dt)
+    if normed is not None and _unfit(normed, dt, (M, K), index):
+        _refuse("normed", normed, dt, (M, K), index)
+    if out is None:
+        out = _act(M, K)
+    else:
+        _check_out(out, M, K, index)
+    _check(_lib.lib.svdq_rms_norm_quantize_w8a8(
+        x_type, x.data_ptr(), ldx, r_addr, ldr, M, K, _addr(norm_weight), eps, _addr(inv_lambda), _addr(h_out),
+        _addr(normed), out.x_codes.data_ptr(), out.x_scales.data_ptr(), _current_stream(index)),
+        "svdq_rms_norm_quantize_w8a8")
+    return (x if h_out is None else h_out), out
 
 
 def gemm_w8a8(q: QuantizedActW8A8, packed: PackedWeightW8A8, y: torch.Tensor | None = None,
@@ -318,21 +345,27 @@ def gemm_w8a8(q: QuantizedActW8A8, packed: PackedWeightW8A8, y: torch.Tensor | N
         raise ValueError(f"out_dtype: expected bf16, fp16 or fp32, got {out_dtype}")
     x_codes, x_scales, w_codes, w_scales = q.x_codes, q.x_scales, packed.w_codes, packed.w_scales
     index = x_codes.get_device()
-    _check_tensor("q.x_codes", x_codes, torch.int8, (M, K), index)
-    _check_tensor("q.x_scales", x_scales, torch.float32, (M,), index)
-    _check_tensor("packed.w_codes", w_codes, torch.int8, (N, K), index)
-    _check_tensor("packed.w_scales", w_scales, torch.float32, (N,), index)
-    if bias is not None:
-        _check_tensor("packed.bias", bias, out_dtype, (N,), index)
-    if y is not None:
-        _check_tensor("y", y, out_dtype, (M, N), index)
-    if index < 0:
-        raise ValueError(f"expected CUDA tensors, got tensors on {x_codes.device}")
+    if _unfit(x_codes, _I8, (M, K), index):
+        _refuse("q.x_codes", x_codes, _I8, (M, K), index)
+    if _unfit(x_scales, _F32, (M,), index):
+        _refuse("q.x_scales", x_scales, _F32, (M,), index)
+    if _unfit(w_codes, _I8, (N, K), index):
+        _refuse("packed.w_codes", w_codes, _I8, (N, K), index)
+    if _unfit(w_scales, _F32, (N,), index):
+        _refuse("packed.w_scales", w_scales, _F32, (N,), index)
+    if bias is not None and _unfit(bias, out_dtype, (N,), index):
+        _refuse("packed.bias", bias, out_dtype, (N,), index)
+    if y is not None and _unfit(y, out_dtype, (M, N), index):
+        _refuse("y", y, out_dtype, (M, N), index)
+    if index != _current_device():
+        if index < 0:
+            raise ValueError(f"expected CUDA tensors, got tensors on {x_codes.device}")
+        return _on_device(index, gemm_w8a8, q, packed, y, out_dtype)
     if y is None:
-        y = torch.empty((M, N), dtype=out_dtype, device=x_codes.device)
-    _call("svdq_gemm_w8a8", index,
-          (x_codes.data_ptr(), x_scales.data_ptr(), M, w_codes.data_ptr(), w_scales.data_ptr(), N, K, _addr(bias),
-           y_type, y.data_ptr()))
+        y = _empty_strided((M, N), (N, 1), out_dtype)
+    _check(_lib.lib.svdq_gemm_w8a8(x_codes.data_ptr(), x_scales.data_ptr(), M, w_codes.data_ptr(),
+                                   w_scales.data_ptr(), N, K, _addr(bias), y_type, y.data_ptr(),
+                                   _current_stream(index)), "svdq_gemm_w8a8")
     return y
 
 
