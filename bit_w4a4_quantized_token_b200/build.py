@@ -1,4 +1,5 @@
-"""Compile the CUDA library (sm_100a) in-tree: libsvdq_b200.so next to this file.
+"""Compile the CUDA library (sm_100a) in-tree, libsvdq_b200.so next to this file,
+and the CPython module beside it that makes the W8A8 layer's calls (_w8a8_front.so).
 
     python -m bit_w4a4_quantized_token_b200.build [--force]
 """
@@ -15,6 +16,8 @@ LIB = os.path.join(_HERE, "libsvdq_b200.so")
 SOURCES = sorted(glob.glob(os.path.join(_HERE, "csrc", "*.cu")) + glob.glob(os.path.join(_HERE, "csrc", "*.cuh"))
                  + [os.path.join(_ROOT, "include", "svdq.h")])
 MAIN = os.path.join(_HERE, "csrc", "svdq_lib.cu")
+FRONT = os.path.join(_HERE, "_w8a8_front.so")
+FRONT_MAIN = os.path.join(_HERE, "csrc", "w8a8_front.cpp")
 
 
 def nvcc_command(out: str = LIB) -> list[str]:
@@ -23,18 +26,38 @@ def nvcc_command(out: str = LIB) -> list[str]:
             "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(_ROOT, "include"), "-o", out, MAIN]
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and os.path.exists(LIB):
-        newest = max(os.path.getmtime(s) for s in SOURCES)
-        if os.path.getmtime(LIB) >= newest:
-            return LIB
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = nvcc_command(tmp)
+def front_command(out: str = FRONT) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I" + os.path.join(_ROOT, "include"), "-I" + sysconfig.get_paths()["include"], "-isystem", inc, "-isystem",
+            os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", "/usr/local/cuda/include", "-o", out,
+            FRONT_MAIN, "-L" + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ltorch",
+            # the C++ runtime that torch has loaded, also where the compiler would link its own statically: streams
+            # and exceptions pass between the two
+            "-l:libstdc++.so.6"]
+
+
+def _compile(out: str, sources: list[str], command, force: bool, verbose: bool) -> str:
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= max(os.path.getmtime(s) for s in sources):
+        return out
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = command(tmp)
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, out)
+    return out
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    _compile(FRONT, [FRONT_MAIN, os.path.join(_ROOT, "include", "svdq.h")], front_command, force, verbose)
+    return _compile(LIB, SOURCES, nvcc_command, force, verbose)
 
 
 if __name__ == "__main__":

@@ -14,11 +14,12 @@ The 8-bit integer (W8A8) layer, for the layers that 4 bits cost too much:
 """
 from __future__ import annotations
 
+import ctypes
 from dataclasses import dataclass, fields
 
 import torch
 
-from . import _lib
+from . import _lib, _w8a8_front as _front
 
 _U8 = torch.uint8
 
@@ -128,7 +129,6 @@ def svdq_linear(x: torch.Tensor, packed: PackedWeight, x_tensor_scale=None, stre
 _DTYPES = {torch.bfloat16: _lib.SVDQ_BF16, torch.float16: _lib.SVDQ_F16, torch.float32: _lib.SVDQ_F32}
 
 
-_I8, _F32 = torch.int8, torch.float32
 
 
 @dataclass(slots=True)
@@ -148,51 +148,15 @@ class QuantizedActW8A8:
     x_scales: torch.Tensor              # fp32 [M]
 
 
-# A call of this layer on few tokens is bound by what the host does for it, so these functions ask torch for the
-# current device and stream without building torch.cuda's objects (3 us for current_stream alone), allocate with the
-# allocator's short form where torch has it (0.7 us a tensor, torch.empty 2.3), test operands in one expression each
-# and put the message together only for a refusal, and call the library with plain addresses.
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-try:
-    from torch._C._dynamo.guards import _empty_strided_cuda as _empty_strided   # (sizes, strides, dtype)
-except ImportError:
-    def _empty_strided(size, stride, dtype):
-        return torch.empty_strided(size, stride, dtype=dtype, device="cuda")
+def _raise_status(status: int, name: str) -> None:
+    raise _lib.SvdqError(status, name)
 
 
-def _unfit(t: torch.Tensor, dtype, shape: tuple, index: int) -> bool:
-    """Whether a contiguous operand is not what the library will take it for behind its pointer."""
-    return t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous()
-
-
-def _refuse(name: str, t: torch.Tensor, dtype, shape: tuple, index: int) -> None:
-    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {index}, got "
-                     f"{t.dtype} {tuple(t.shape)} (strides {t.stride()}) on {t.device}")
-
-
-def _rows(name: str, x: torch.Tensor, K: int) -> tuple[int, int, int]:
-    """(library's type, rows, row stride) of a matrix of activations; rows may be apart, elements of a row not."""
-    x_type, shape, strides = _DTYPES.get(x.dtype), x.shape, x.stride()
-    if x_type is None or len(shape) != 2 or shape[1] != K or strides[1] != 1 or not x.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA matrix [M, {K}] of bf16, fp16 or fp32 with contiguous rows, got "
-                         f"{x.dtype} {tuple(shape)} (strides {strides}) on {x.device}")
-    return x_type, shape[0], (strides[0] if shape[0] > 1 else K)
-
-
-def _addr(t: torch.Tensor | None) -> int | None:
-    return None if t is None else t.data_ptr()
-
-
-def _check(status: int, name: str) -> None:
-    if status:
-        raise _lib.SvdqError(status, name)
-
-
-def _on_device(index: int, fn, *args):
-    """fn(*args) with GPU `index` current: where the operands are is where everything happens."""
-    with torch.cuda.device(index):
-        return fn(*args)
+# The operands' checks, the outputs' allocation and the library call are one call of a small native module: a layer
+# call on few tokens is bound by what the host does for it, and in Python that was twice the GPU's time.
+_front.bind(*(ctypes.cast(getattr(_lib.lib, name), ctypes.c_void_p).value
+              for name in ("svdq_pack_weight_w8a8", "svdq_quantize_act_w8a8", "svdq_rms_norm_quantize_w8a8",
+                           "svdq_gemm_w8a8")), _raise_status)
 
 
 def _tensors(v):
@@ -229,41 +193,19 @@ def pack_weight_w8a8(W: torch.Tensor, lam: torch.Tensor | None = None, bias: tor
     lam [K] (fp32) the rows W * lam are quantised and activations are divided by lam."""
     if stream is not None:
         return _on_stream(stream, W, pack_weight_w8a8, W, lam, bias)
+    w_codes, w_scales, inv_lambda = _front.pack(W, lam)
     N, K = W.shape
-    w_type = _rows("W", W, K)[0]
-    W = W.contiguous()
-    dev, index = W.device, W.get_device()
-    if lam is not None and _unfit(lam, _F32, (K,), index):
-        _refuse("lam", lam, _F32, (K,), index)
-    if bias is not None and (bias.shape != (N,) or bias.dtype not in _DTYPES or bias.get_device() != index):
-        raise ValueError(f"bias: expected a bf16, fp16 or fp32 tensor of shape ({N},) on {dev}, got {bias.dtype} "
-                         f"{tuple(bias.shape)} on {bias.device}")
-    if index != _current_device():
-        return _on_device(index, pack_weight_w8a8, W, lam, bias)
-    w_codes = torch.empty(N, K, dtype=_I8, device=dev)
-    w_scales = torch.empty(N, dtype=_F32, device=dev)
-    inv_lambda = torch.empty(K, dtype=_F32, device=dev) if lam is not None else None
-    _check(_lib.lib.svdq_pack_weight_w8a8(w_type, W.data_ptr(), N, K, _addr(lam), w_codes.data_ptr(),
-                                          w_scales.data_ptr(), _addr(inv_lambda), _current_stream(index)),
-           "svdq_pack_weight_w8a8")
-    return PackedWeightW8A8(N, K, w_codes, w_scales, inv_lambda, None if bias is None else bias.contiguous())
+    if bias is not None:
+        if bias.shape != (N,) or bias.dtype not in _DTYPES or bias.device != W.device:
+            raise ValueError(f"bias: expected a bf16, fp16 or fp32 tensor of shape ({N},) on {W.device}, got "
+                             f"{bias.dtype} {tuple(bias.shape)} on {bias.device}")
+        bias = bias.contiguous()
+    return PackedWeightW8A8(N, K, w_codes, w_scales, inv_lambda, bias)
 
 
 def alloc_act_w8a8(packed: PackedWeightW8A8, M: int, device) -> QuantizedActW8A8:
-    return QuantizedActW8A8(M, torch.empty(M, packed.K, dtype=_I8, device=device),
-                            torch.empty(M, dtype=_F32, device=device))
-
-
-def _act(M: int, K: int) -> QuantizedActW8A8:
-    """alloc_act_w8a8 on the current GPU."""
-    return QuantizedActW8A8(M, _empty_strided((M, K), (K, 1), _I8), _empty_strided((M,), (1,), _F32))
-
-
-def _check_out(out: QuantizedActW8A8, M: int, K: int, index: int) -> None:
-    if _unfit(out.x_codes, _I8, (M, K), index):
-        _refuse("out.x_codes", out.x_codes, _I8, (M, K), index)
-    if _unfit(out.x_scales, _F32, (M,), index):
-        _refuse("out.x_scales", out.x_scales, _F32, (M,), index)
+    return QuantizedActW8A8(M, torch.empty(M, packed.K, dtype=torch.int8, device=device),
+                            torch.empty(M, dtype=torch.float32, device=device))
 
 
 def quantize_act_w8a8(x: torch.Tensor, packed: PackedWeightW8A8, out: QuantizedActW8A8 | None = None,
@@ -271,20 +213,10 @@ def quantize_act_w8a8(x: torch.Tensor, packed: PackedWeightW8A8, out: QuantizedA
     """x [M, K] bf16, fp16 or fp32 (rows may be apart) -> 8-bit codes and a scale per token."""
     if stream is not None:
         return _on_stream(stream, x, quantize_act_w8a8, x, packed, out)
-    K, inv_lambda = packed.K, packed.inv_lambda
-    x_type, M, ldx = _rows("x", x, K)
-    index = x.get_device()
-    if index != _current_device():
-        return _on_device(index, quantize_act_w8a8, x, packed, out)
-    if inv_lambda is not None and _unfit(inv_lambda, _F32, (K,), index):
-        _refuse("packed.inv_lambda", inv_lambda, _F32, (K,), index)
-    if out is None:
-        out = _act(M, K)
-    else:
-        _check_out(out, M, K, index)
-    _check(_lib.lib.svdq_quantize_act_w8a8(x_type, x.data_ptr(), ldx, M, K, _addr(inv_lambda), out.x_codes.data_ptr(),
-                                           out.x_scales.data_ptr(), _current_stream(index)), "svdq_quantize_act_w8a8")
-    return out
+    if out is not None:
+        _front.quantize(x, packed.K, packed.inv_lambda, out.x_codes, out.x_scales)
+        return out
+    return QuantizedActW8A8(*_front.quantize(x, packed.K, packed.inv_lambda, None, None))
 
 
 def rms_norm_quantize_w8a8(x: torch.Tensor, residual: torch.Tensor | None, norm_weight: torch.Tensor | None,
@@ -297,38 +229,10 @@ def rms_norm_quantize_w8a8(x: torch.Tensor, residual: torch.Tensor | None, norm_
     if stream is not None:
         return _on_stream(stream, x, rms_norm_quantize_w8a8, x, residual, norm_weight, packed, eps, h_out, normed,
                           out)
-    K, inv_lambda = packed.K, packed.inv_lambda
-    x_type, M, ldx = _rows("x", x, K)
-    index, dt = x.get_device(), x.dtype
-    if index != _current_device():
-        return _on_device(index, rms_norm_quantize_w8a8, x, residual, norm_weight, packed, eps, h_out, normed, out)
-    ldr, r_addr = K, None
-    if residual is not None:
-        r_type, r_rows, ldr = _rows("residual", residual, K)
-        if r_type != x_type or r_rows != M or residual.get_device() != index:
-            raise ValueError(f"residual: expected {dt} {(M, K)} on {x.device}, got {residual.dtype} "
-                             f"{tuple(residual.shape)} on {residual.device}")
-        r_addr = residual.data_ptr()
-    if norm_weight is not None and _unfit(norm_weight, dt, (K,), index):
-        _refuse("norm_weight", norm_weight, dt, (K,), index)
-    if inv_lambda is not None and _unfit(inv_lambda, _F32, (K,), index):
-        _refuse("packed.inv_lambda", inv_lambda, _F32, (K,), index)
-    if h_out is not None:
-        if _unfit(h_out, dt, (M, K), index):
-            _refuse("h_out", h_out, dt, (M, K), index)
-    elif residual is not None:
-        h_out = _empty_strided((M, K), (K, 1), dt)
-    if normed is not None and _unfit(normed, dt, (M, K), index):
-        _refuse("normed", normed, dt, (M, K), index)
-    if out is None:
-        out = _act(M, K)
-    else:
-        _check_out(out, M, K, index)
-    _check(_lib.lib.svdq_rms_norm_quantize_w8a8(
-        x_type, x.data_ptr(), ldx, r_addr, ldr, M, K, _addr(norm_weight), eps, _addr(inv_lambda), _addr(h_out),
-        _addr(normed), out.x_codes.data_ptr(), out.x_scales.data_ptr(), _current_stream(index)),
-        "svdq_rms_norm_quantize_w8a8")
-    return (x if h_out is None else h_out), out
+    codes, scales = (None, None) if out is None else (out.x_codes, out.x_scales)
+    h, M, codes, scales = _front.norm(x, residual, norm_weight, packed.K, packed.inv_lambda, eps, h_out, normed,
+                                      codes, scales)
+    return h, (QuantizedActW8A8(M, codes, scales) if out is None else out)
 
 
 def gemm_w8a8(q: QuantizedActW8A8, packed: PackedWeightW8A8, y: torch.Tensor | None = None,
@@ -337,36 +241,13 @@ def gemm_w8a8(q: QuantizedActW8A8, packed: PackedWeightW8A8, y: torch.Tensor | N
     else bf16); the bias has that type too."""
     if stream is not None:
         return _on_stream(stream, q.x_codes, gemm_w8a8, q, packed, y, out_dtype)
-    M, N, K, bias = q.M, packed.N, packed.K, packed.bias
+    bias = packed.bias
     if out_dtype is None:
         out_dtype = y.dtype if y is not None else bias.dtype if bias is not None else torch.bfloat16
     y_type = _DTYPES.get(out_dtype)
     if y_type is None:
         raise ValueError(f"out_dtype: expected bf16, fp16 or fp32, got {out_dtype}")
-    x_codes, x_scales, w_codes, w_scales = q.x_codes, q.x_scales, packed.w_codes, packed.w_scales
-    index = x_codes.get_device()
-    if _unfit(x_codes, _I8, (M, K), index):
-        _refuse("q.x_codes", x_codes, _I8, (M, K), index)
-    if _unfit(x_scales, _F32, (M,), index):
-        _refuse("q.x_scales", x_scales, _F32, (M,), index)
-    if _unfit(w_codes, _I8, (N, K), index):
-        _refuse("packed.w_codes", w_codes, _I8, (N, K), index)
-    if _unfit(w_scales, _F32, (N,), index):
-        _refuse("packed.w_scales", w_scales, _F32, (N,), index)
-    if bias is not None and _unfit(bias, out_dtype, (N,), index):
-        _refuse("packed.bias", bias, out_dtype, (N,), index)
-    if y is not None and _unfit(y, out_dtype, (M, N), index):
-        _refuse("y", y, out_dtype, (M, N), index)
-    if index != _current_device():
-        if index < 0:
-            raise ValueError(f"expected CUDA tensors, got tensors on {x_codes.device}")
-        return _on_device(index, gemm_w8a8, q, packed, y, out_dtype)
-    if y is None:
-        y = _empty_strided((M, N), (N, 1), out_dtype)
-    _check(_lib.lib.svdq_gemm_w8a8(x_codes.data_ptr(), x_scales.data_ptr(), M, w_codes.data_ptr(),
-                                   w_scales.data_ptr(), N, K, _addr(bias), y_type, y.data_ptr(),
-                                   _current_stream(index)), "svdq_gemm_w8a8")
-    return y
+    return _front.gemm(q.x_codes, q.x_scales, q.M, packed.w_codes, packed.w_scales, packed.N, packed.K, bias, y_type, y)
 
 
 def w8a8_linear(x: torch.Tensor, packed: PackedWeightW8A8, out_dtype: torch.dtype | None = None,
