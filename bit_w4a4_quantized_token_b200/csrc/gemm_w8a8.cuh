@@ -27,6 +27,7 @@ struct GemmW8Args {
     int chunks;              // ceil(K / 128): stages of 128 bytes of K
     int last_steps;          // 32-byte K-steps of the last chunk (1..4)
     int m_tiles, n_tiles;
+    int group_m;             // pair kernel: row tiles that are walked together
     int stages;              // narrow kernel: ring depth
 };
 
@@ -83,19 +84,18 @@ constexpr size_t COL_OFF = BOX_OFF + (size_t)kEpiWarps * kBoxBytes;
 constexpr size_t SMEM_BYTES = 1024 + COL_OFF + (size_t)kEpiWarps * 2 * kColBytes;
 static_assert((2 * kStages + 4) * 8 + 4 <= 1024, "barriers do not fit");
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
-constexpr int kGroupM = 8;                    // row tiles that are walked together (below)
 }  // namespace w8p
 
-// Tile of a running index: groups of kGroupM row tiles, the row tile fastest,
-// so that the ~74 tiles in flight form a block of about 8 x 9 and share their
-// operands in the L2 (a row-major walk keeps 74 different weight tiles in
-// flight and re-reads the whole weight for every row tile).
-__device__ __forceinline__ void w8_tile(int id, int m_tiles, int n_tiles, int& m, int& n) {
-    const int per_group = w8p::kGroupM * n_tiles;
+// Tile of a running index: groups of group_m row tiles, the row tile fastest,
+// so that the ~74 tiles in flight form a block that shares its operands in the
+// L2 (a row-major walk keeps 74 different weight tiles in flight and re-reads
+// the whole weight for every row tile).
+__device__ __forceinline__ void w8_tile(int id, const GemmW8Args& a, int& m, int& n) {
+    const int per_group = a.group_m * a.n_tiles;
     const int g = id / per_group, in = id - g * per_group;
-    const int gm = min(w8p::kGroupM, m_tiles - g * w8p::kGroupM);
+    const int gm = min(a.group_m, a.m_tiles - g * a.group_m);
     n = in / gm;
-    m = g * w8p::kGroupM + (in - n * gm);
+    m = g * a.group_m + (in - n * gm);
 }
 
 template <int OUT>
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
     // kernel ends (only into the L2: that kernel may have written them)
     if (warp >= (uint32_t)kEpiWarp0 && lane == 0) {
         int m, n;
-        w8_tile(cluster, a.m_tiles, a.n_tiles, m, n);
+        w8_tile(cluster, a, m, n);
         const int c = (int)warp - kEpiWarp0;
         if (c < min(a.chunks, kStages * kPer)) tma_prefetch_l2_2d(&tm_w, c * BK, n * BN + 128 * (int)rank);
     }
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
             bool ok = true;
             for (int id = cluster; id < total && ok; id += n_clusters) {
                 int m, n;
-                w8_tile(id, a.m_tiles, a.n_tiles, m, n);
+                w8_tile(id, a, m, n);
                 const int row0 = (is_x ? m * BM : n * BN) + 128 * (int)rank;
                 for (int c = 0; c < a.chunks; c += kPer) {
                     if (!bounded_wait(&empty[s], ph, kSiteW8Empty)) {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
         int local = 0;
         for (int id = cluster; id < total; id += n_clusters, ++local) {
             int mt, nt;
-            w8_tile(id, a.m_tiles, a.n_tiles, mt, nt);
+            w8_tile(id, a, mt, nt);
             const int row0 = mt * BM + 128 * (int)rank + 32 * (int)q;   // the warp's first token
             const int row = row0 + (int)lane;
             const int n0 = nt * BN + 128 * half;
