@@ -928,14 +928,16 @@ W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
     if (mode == 2) return best;
     constexpr int kNt[4] = {16, 32, 64, 128}, kChunkNs[4] = {150, 150, 224, 316};
     // CTAs of a split that are resident at once: clusters of 4 and 8 leave SMs
-    // of a GPC unused (33 and 15 of them fit 148 SMs)
+    // of a GPC unused (33 and 15 of them fit 148 SMs).  16 tokens, N = 2560, K =
+    // 13824: 20 tiles split in four 11.2 us, in eight (160 CTAs) 14.8.
     const int slots[4] = {sms, sms / 2 * 2, sms * 132 / 148, sms * 120 / 148};
     for (int i = 0; i < 4; ++i) {
         const int nt = kNt[i];
         const int64_t mt = (M + nt - 1) / nt, ntl = (N + w8n::BN - 1) / w8n::BN;
         if (mt > 65535 || ntl > 65535) continue;   // the grid's limits
         for (int l = 0; l < 4 && (1 << l) <= chunks; ++l) {
-            const int64_t waves = (((mt * ntl) << l) + slots[l] - 1) / slots[l];
+            const int64_t ctas = (mt * ntl) << l, waves = (ctas + slots[l] - 1) / slots[l];
+            if (l > 0 && waves > 1) break;   // a second wave of clusters costs more than a split saves
             const int64_t of_cta = (chunks + (1 << l) - 1) >> l;
             int64_t ns = 2650 + load(waves * of_cta * kChunkNs[i]);
             if (l > 0) ns += 1050 + 96 * ((std::min<int64_t>(M, nt) + (1 << l) - 1) >> l);
