@@ -10,6 +10,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "svdq.h"
@@ -74,8 +75,8 @@ bool g_device_ready[kMaxDevices];
 // Budget of dynamic shared memory for the activation quantizer (the opt-in
 // maximum is 227 KB per block including static shared memory).
 constexpr int kQuantSmemBudget = 226 * 1024;
-// The same for the narrow W8A8 GEMM when one block runs per SM.
-constexpr int kNarrowSmemBudget = 224 * 1024;
+// The same for the ring buffers of the W8A8 kernels, with room for their static shared memory.
+constexpr int kW8SmemBudget = 224 * 1024;
 
 thread_local char g_last_error[256] = "";
 
@@ -100,9 +101,9 @@ svdq_status launch_status(const char* where) {
 template <int NT>
 bool set_narrow_limits() {
     const cudaFuncAttribute attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
-    return cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kBf16>, attr, kNarrowSmemBudget) == cudaSuccess &&
-           cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kF16>, attr, kNarrowSmemBudget) == cudaSuccess &&
-           cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kF32>, attr, kNarrowSmemBudget) == cudaSuccess;
+    return cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kBf16>, attr, kW8SmemBudget) == cudaSuccess &&
+           cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kF16>, attr, kW8SmemBudget) == cudaSuccess &&
+           cudaFuncSetAttribute(gemm_w8a8_narrow_kernel<NT, kF32>, attr, kW8SmemBudget) == cudaSuccess;
 }
 
 // Rejects anything but compute capability 10.0 before any launch, and sets
@@ -783,10 +784,24 @@ svdq_status check_stride(int64_t ld, int64_t K, svdq_dtype t) {
     return SVDQ_OK;
 }
 
-// Whether the byte ranges [p, p + np) and [q, q + nq) share memory.
-bool overlaps(const void* p, int64_t np, const void* q, int64_t nq) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-    return p != nullptr && q != nullptr && a < b + (uintptr_t)nq && b < a + (uintptr_t)np;
+// A range of memory; none when p is null.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && x < y + (uintptr_t)b.bytes && y < x + (uintptr_t)a.bytes;
+}
+// Whether an output shares memory with an input or with another output.
+bool any_overlap(std::initializer_list<Span> inputs, std::initializer_list<Span> outputs) {
+    for (const Span* o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span& i : inputs)
+            if (overlap(i, *o)) return true;
+        for (const Span* other = outputs.begin(); other != o; ++other)
+            if (overlap(*other, *o)) return true;
+    }
+    return false;
 }
 
 // Blocks of `threads` threads and `smem` bytes of dynamic shared memory that one SM holds (`slot`: looked up
@@ -831,14 +846,14 @@ svdq_status quantize_rows_ring(const QuantRowsArgs& a, int blocks, cudaStream_t 
     const int dev = current_device();
     static std::atomic<bool> ready[kMaxDevices];
     if (!ready[dev].load()) {
-        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmemBudget) !=
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kW8SmemBudget) !=
             cudaSuccess)
             return cuda_fail("setting the W8A8 row quantizer's shared memory");
         ready[dev].store(true);
     }
     const int threads = (int)round_up((a.K / 8 + q8::kRingVec - 1) / q8::kRingVec, 32);
     const int64_t stage = (int64_t)a.K * (T == kF32 ? 4 : 2) * (a.residual ? 2 : 1);
-    const int64_t stages = std::min<int64_t>((kNarrowSmemBudget / blocks - kRingSlack) / stage, q8::kMaxRing);
+    const int64_t stages = std::min<int64_t>((kW8SmemBudget / blocks - kRingSlack) / stage, q8::kMaxRing);
     if (stages < 2) return SVDQ_ERR_UNSUPPORTED_SHAPE;   // the caller's choice of blocks leaves room for two
     const size_t smem = q8::kRingBarBytes + (size_t)(stages * stage);
     // the blocks that are resident at once share the rows (registers may allow fewer than asked for)
@@ -865,9 +880,9 @@ svdq_status quantize_rows_typed(const QuantRowsArgs& a, cudaStream_t st) {
     const int64_t stage = (int64_t)a.K * (T == kF32 ? 4 : 2) * (a.residual ? 2 : 1);
     const bool held_f32 = T == kF32 && NORM && nvec <= q8::kMaxThreads;
     if (stage >= 16384 && !held_f32 && nvec <= 2 * q8::kRingThreads &&
-        2 * stage + kRingSlack <= kNarrowSmemBudget) {
+        2 * stage + kRingSlack <= kW8SmemBudget) {
         int blocks = nvec <= 512 ? 4 : 2;
-        while (blocks > 1 && 2 * stage + kRingSlack > kNarrowSmemBudget / blocks) blocks /= 2;
+        while (blocks > 1 && 2 * stage + kRingSlack > kW8SmemBudget / blocks) blocks /= 2;
         if (stage >= 32768 && a.M >= 16 * num_sms()) blocks = 1;
         return quantize_rows_ring<T, NORM>(a, blocks, st);
     }
@@ -897,7 +912,7 @@ struct W8Plan {
 // barrier that it waits on: parities repeat).
 int w8_ring(int nt, int split, int64_t chunks) {
     const int64_t most = ((chunks + split - 1) / split + w8n::per(nt) - 1) / w8n::per(nt);
-    const int64_t room = (kNarrowSmemBudget - w8n::fixed_bytes(nt, split)) / w8n::stage_bytes(nt);
+    const int64_t room = (kW8SmemBudget - w8n::fixed_bytes(nt, split)) / w8n::stage_bytes(nt);
     if (most == 1) return 1;
     return (int)(std::min<int64_t>({(int64_t)w8n::kMaxStages, room, most + 1}) / 2 * 2);
 }
@@ -955,7 +970,7 @@ svdq_status gemm_w8a8_narrow(const W8Plan& p, const CUtensorMap& tm_x, const CUt
                              svdq_dtype out, cudaStream_t st) {
     a.stages = p.stages;
     const size_t smem = (size_t)w8n::fixed_bytes(NT, p.split) + (size_t)p.stages * w8n::stage_bytes(NT);
-    if (p.stages < 1 || smem > (size_t)kNarrowSmemBudget) return SVDQ_ERR_UNSUPPORTED_SHAPE;   // no plan is so
+    if (p.stages < 1 || smem > (size_t)kW8SmemBudget) return SVDQ_ERR_UNSUPPORTED_SHAPE;   // no plan is so
     const dim3 grid((unsigned)p.split, (unsigned)a.n_tiles, (unsigned)a.m_tiles);
     const auto kernel = out == SVDQ_F32   ? gemm_w8a8_narrow_kernel<NT, kF32>
                         : out == SVDQ_F16 ? gemm_w8a8_narrow_kernel<NT, kF16>
@@ -1498,6 +1513,9 @@ svdq_status svdq_pack_weight_w8a8(svdq_dtype w_type, const void* W, int64_t N, i
     SVDQ_TRY(check_ptr(w_scales));
     SVDQ_TRY(check_opt_ptr(lambda));
     SVDQ_TRY(lambda ? check_ptr(inv_lambda) : check_opt_ptr(inv_lambda));
+    if (any_overlap({{W, N * K * dtype_bytes(w_type)}, {lambda, 4 * K}},
+                    {{w_codes, N * K}, {w_scales, 4 * N}, {lambda ? inv_lambda : nullptr, 4 * K}}))
+        return SVDQ_ERR_INVALID_ARG;
     SVDQ_TRY(check_device());
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (lambda) SVDQ_TRY(fold_lowrank(lambda, nullptr, nullptr, N, K, 0, inv_lambda, nullptr, nullptr, st));
@@ -1521,7 +1539,9 @@ svdq_status svdq_quantize_act_w8a8(svdq_dtype x_type, const void* x, int64_t ldx
     SVDQ_TRY(check_opt_ptr(inv_lambda));
     SVDQ_TRY(check_ptr(x_codes));
     SVDQ_TRY(check_ptr(x_scales));
-    if (overlaps(x, ((M - 1) * ldx + K) * dtype_bytes(x_type), x_codes, M * K)) return SVDQ_ERR_INVALID_ARG;
+    if (any_overlap({{x, ((M - 1) * ldx + K) * dtype_bytes(x_type)}, {inv_lambda, 4 * K}},
+                    {{x_codes, M * K}, {x_scales, 4 * M}}))
+        return SVDQ_ERR_INVALID_ARG;
     SVDQ_TRY(check_device());
     QuantRowsArgs a = {};
     a.x = x;
@@ -1556,16 +1576,14 @@ svdq_status svdq_rms_norm_quantize_w8a8(svdq_dtype x_type, const void* x, int64_
     // an output may share memory with an input only as h_out does in place:
     // the same rows at the same addresses
     const int64_t b = dtype_bytes(x_type), out_bytes = M * K * b;
-    const int64_t x_bytes = ((M - 1) * ldx + K) * b, r_bytes = ((M - 1) * ldr + K) * b;
-    const bool h_on_x = h_out == x && (ldx == K || M == 1);
-    const bool h_on_r = h_out == residual && (ldr == K || M == 1);
-    if ((!h_on_x && overlaps(h_out, out_bytes, x, x_bytes)) ||
-        (!h_on_r && residual && overlaps(h_out, out_bytes, residual, r_bytes)) ||
-        overlaps(normed, out_bytes, x, x_bytes) || (residual && overlaps(normed, out_bytes, residual, r_bytes)) ||
-        overlaps(x_codes, M * K, x, x_bytes) || (residual && overlaps(x_codes, M * K, residual, r_bytes)) ||
-        overlaps(normed, out_bytes, h_out, out_bytes) || overlaps(x_codes, M * K, h_out, out_bytes) ||
-        overlaps(x_codes, M * K, normed, out_bytes))
+    const Span in_x = {x, ((M - 1) * ldx + K) * b}, in_r = {residual, residual ? ((M - 1) * ldr + K) * b : 0};
+    const Span out_h = {h_out, out_bytes};
+    if (any_overlap({in_x, in_r, {norm_weight, K * b}, {inv_lambda, 4 * K}, out_h},
+                    {{normed, out_bytes}, {x_codes, M * K}, {x_scales, 4 * M}}) ||
+        any_overlap({{norm_weight, K * b}, {inv_lambda, 4 * K}}, {out_h}))
         return SVDQ_ERR_INVALID_ARG;
+    const bool h_on_x = h_out == x && (ldx == K || M == 1), h_on_r = h_out == residual && (ldr == K || M == 1);
+    if ((!h_on_x && overlap(in_x, out_h)) || (!h_on_r && overlap(in_r, out_h))) return SVDQ_ERR_INVALID_ARG;
     SVDQ_TRY(check_device());
     QuantRowsArgs a = {};
     a.x = x;
@@ -1597,6 +1615,10 @@ svdq_status svdq_gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M
     SVDQ_TRY(check_ptr(w_scales));
     SVDQ_TRY(check_opt_ptr(bias));
     SVDQ_TRY(check_ptr(y));
+    const int64_t b = dtype_bytes(y_type);
+    if (any_overlap({{x_codes, M * K}, {x_scales, 4 * M}, {w_codes, N * K}, {w_scales, 4 * N}, {bias, N * b}},
+                    {{y, M * N * b}}))
+        return SVDQ_ERR_INVALID_ARG;
     SVDQ_TRY(check_device());
     return gemm_w8a8(x_codes, x_scales, M, w_codes, w_scales, N, K, bias, y_type, y,
                      reinterpret_cast<cudaStream_t>(stream));

@@ -370,6 +370,8 @@ svdq_status svdq_gemm_w4a16(const void* x, int64_t M, const void* w_codes, const
  * Layouts: codes [rows, K] int8, row-major; scales [rows] fp32; K needs no
  * padding.  Sizes: 1 <= rows < 2^31; 16 <= K < 2^17, K % 16 == 0 (the int32
  * sum cannot overflow, whatever the codes); N % 8 == 0.
+ * No output may share memory with an input or another output, but for h_out in
+ * place (below): INVALID_ARG.
  * Tensors that are quantised or stored have one of these types: */
 typedef enum { SVDQ_BF16 = 0, SVDQ_F16 = 1, SVDQ_F32 = 2 } svdq_dtype;
 
@@ -390,7 +392,7 @@ svdq_status svdq_pack_weight_w8a8(svdq_dtype w_type, const void* W, int64_t N, i
  *   x           device x_type [M, K], rows ldx elements apart (ldx >= K, a
  *               multiple of 16 bytes; elements of a row contiguous)
  *   inv_lambda  device fp32 [K] or NULL (no smoothing)
- * Outputs: x_codes [M, K], x_scales fp32 [M] (not in x's memory).
+ * Outputs: x_codes [M, K], x_scales fp32 [M].
  * Errors: INVALID_ARG, UNSUPPORTED_SHAPE (sizes, ldx), UNSUPPORTED_DEVICE, CUDA. */
 svdq_status svdq_quantize_act_w8a8(svdq_dtype x_type, const void* x, int64_t ldx, int64_t M, int64_t K,
                                    const float* inv_lambda, void* x_codes, float* x_scales, svdq_stream_t stream);
@@ -413,9 +415,8 @@ svdq_status svdq_quantize_act_w8a8(svdq_dtype x_type, const void* x, int64_t ldx
  *            example svdq_quantize_act)
  *   x_codes [M, K], x_scales fp32 [M]: both or neither; at least one of
  *   {codes and scales, normed} must be given.
- * Errors: INVALID_ARG (pointers, eps, outputs that overlap each other or an
- * input other than as h_out in place), UNSUPPORTED_SHAPE (sizes, strides),
- * UNSUPPORTED_DEVICE, CUDA. */
+ * Errors: INVALID_ARG (pointers, eps, overlaps), UNSUPPORTED_SHAPE (sizes,
+ * strides), UNSUPPORTED_DEVICE, CUDA. */
 svdq_status svdq_rms_norm_quantize_w8a8(svdq_dtype x_type, const void* x, int64_t ldx, const void* residual,
                                         int64_t ldr, int64_t M, int64_t K, const void* norm_weight, float eps,
                                         const float* inv_lambda, void* h_out, void* normed, void* x_codes,

@@ -465,6 +465,112 @@ def test_two_streams_at_once():
         assert all(torch.equal(g, want[i]) for g in got[i])
 
 
+@pytest.mark.parametrize("M,K,layers", [(1, 1024, 12), (40, 2048, 12), (700, 2048, 6), (3000, 1024, 6)])
+def test_layer_after_layer_without_waiting(M, K, layers):
+    """Each kernel starts while the one before it ends: a stack of layers run without a wait between the calls
+    equals the same stack with a wait after each, in place on the same residual stream and buffers."""
+    from bit_w4a4_quantized_token_b200 import layer
+
+    weights = [layer.pack_weight_w8a8((torch.randn(K, K, generator=torch.Generator().manual_seed(i)) / K ** 0.5)
+                                      .to(BF16).cuda(), uniform(K, 0.5, 2.0, i).cuda()) for i in range(layers)]
+    w = uniform(K, 0.5, 2.0, 99, BF16).cuda()
+    x0, r0 = draw(M, K, BF16, 1).cuda(), draw(M, K, BF16, 2).cuda()
+
+    def stack(wait):
+        x, r = x0.clone(), r0.clone()
+        q = layer.alloc_act_w8a8(weights[0], M, x.device)
+        for p in weights:
+            layer.rms_norm_quantize_w8a8(x, r, w, p, h_out=r, out=q)
+            if wait:
+                torch.cuda.synchronize()
+            layer.gemm_w8a8(q, p, y=x)
+            if wait:
+                torch.cuda.synchronize()
+            layer.quantize_act_w8a8(x, p, out=q)
+            if wait:
+                torch.cuda.synchronize()
+            layer.gemm_w8a8(q, p, y=x)
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return x, r
+
+    want = stack(True)
+    assert bool(torch.isfinite(want[0]).all())
+    for _ in range(3):
+        got = stack(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+FIRST_CALL_IN_CAPTURE = """
+import torch
+from bit_w4a4_quantized_token_b200 import layer
+x = torch.randn(70, 512, device="cuda").bfloat16()
+codes = torch.randint(-127, 128, (264, 512), dtype=torch.int8, device="cuda")
+p = layer.PackedWeightW8A8(264, 512, codes, torch.rand(264, device="cuda"), None, None)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    h, q = layer.rms_norm_quantize_w8a8(x, x, None, p)
+    y = layer.gemm_w8a8(q, p)
+    z = layer.w8a8_linear(x, p)
+g.replay()
+torch.cuda.synchronize()
+h2, q2 = layer.rms_norm_quantize_w8a8(x, x, None, p)
+assert torch.equal(h, h2) and torch.equal(y, layer.gemm_w8a8(q2, p)) and torch.equal(z, layer.w8a8_linear(x, p))
+print("captured")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_CAPTURE], cwd=root, capture_output=True, text=True,
+                       timeout=300, env=dict(os.environ, PYTHONPATH=root))
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_refusals_of_tensors_on_the_gpu():
+    """No rows, rows that start off a 16-byte boundary, rows that overlap one another, other widths and types."""
+    from bit_w4a4_quantized_token_b200 import _lib, layer
+
+    packed = packed_for(64)
+    wide = torch.zeros(8, 80, dtype=BF16, device="cuda")
+    for x, status in ((wide[:0, :64], _lib.SVDQ_ERR_UNSUPPORTED_SHAPE), (wide[:, 1:65], _lib.SVDQ_ERR_INVALID_ARG),
+                      (wide[:1, :64].expand(8, 64), _lib.SVDQ_ERR_UNSUPPORTED_SHAPE),
+                      (torch.zeros(8, 68, dtype=BF16, device="cuda")[:, :64], _lib.SVDQ_ERR_UNSUPPORTED_SHAPE)):
+        for call in (lambda: layer.quantize_act_w8a8(x, packed),
+                     lambda: layer.rms_norm_quantize_w8a8(x, None, None, packed)):
+            with pytest.raises(_lib.SvdqError) as e:
+                call()
+            assert e.value.status == status
+    x = wide[:, :64].contiguous()
+    for bad in (dict(residual=x.half()), dict(residual=x[:4]), dict(residual=x.cpu()), dict(norm_weight=x[0].float()),
+                dict(norm_weight=x[0, :32]), dict(h_out=x[:, :32]), dict(normed=x.float()),
+                dict(out=layer.alloc_act_w8a8(packed, 7, x.device))):
+        kw = dict(dict(residual=None, norm_weight=None), **bad)
+        with pytest.raises(ValueError):
+            layer.rms_norm_quantize_w8a8(x, kw.pop("residual"), kw.pop("norm_weight"), packed, **kw)
+    with pytest.raises(_lib.SvdqError):
+        layer.rms_norm_quantize_w8a8(x, None, None, packed, eps=0.0)
+    q = layer.quantize_act_w8a8(x, packed)
+    for bad in (dict(y=torch.empty(8, 8, device="cuda").t()[::2]), dict(y=torch.empty(8, 16, dtype=BF16, device="cuda")),
+                dict(out_dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            layer.gemm_w8a8(q, packed, **bad)
+    with pytest.raises(ValueError):
+        layer.gemm_w8a8(layer.QuantizedActW8A8(8, q.x_codes, q.x_scales.cpu()), packed)
+    # an odd number of channels is refused by the library
+    odd = layer.PackedWeightW8A8(7, 64, torch.zeros(7, 64, dtype=torch.int8, device="cuda"),
+                                 torch.zeros(7, device="cuda"), None, None)
+    with pytest.raises(_lib.SvdqError) as e:
+        layer.gemm_w8a8(q, odd)
+    assert e.value.status == _lib.SVDQ_ERR_UNSUPPORTED_SHAPE
+
+
 def test_same_call_twice_gives_the_same_bits():
     from bit_w4a4_quantized_token_b200 import layer
 

@@ -76,12 +76,12 @@ def _status(L, fn, **kw):
         return e.status
 
 
-GEMM = dict(x_codes=FAKE, x_scales=FAKE, M=64, w_codes=FAKE, w_scales=FAKE, N=256, K=256, bias=None, y_type=0, y=FAKE,
+GEMM = dict(x_codes=FAKE, x_scales=FAKE, M=64, w_codes=FAKE, w_scales=FAKE, N=256, K=256, bias=None, y_type=0, y=BIG,
             stream=0)
-QUANT = dict(x_type=0, x=FAKE, ldx=256, M=64, K=256, inv_lambda=None, x_codes=BIG, x_scales=BIG, stream=0)
-PACK = dict(w_type=0, W=FAKE, N=256, K=256, lam=None, w_codes=BIG, w_scales=BIG, inv_lambda=None, stream=0)
-NORM = dict(x_type=0, x=FAKE, ldx=256, residual=2 * BIG, ldr=256, M=64, K=256, norm_weight=FAKE, eps=1e-6,
-            inv_lambda=FAKE, h_out=3 * BIG, normed=4 * BIG, x_codes=5 * BIG, x_scales=6 * BIG, stream=0)
+QUANT = dict(x_type=0, x=FAKE, ldx=256, M=64, K=256, inv_lambda=None, x_codes=BIG, x_scales=2 * BIG, stream=0)
+PACK = dict(w_type=0, W=FAKE, N=256, K=256, lam=None, w_codes=BIG, w_scales=2 * BIG, inv_lambda=None, stream=0)
+NORM = dict(x_type=0, x=FAKE, ldx=256, residual=2 * BIG, ldr=256, M=64, K=256, norm_weight=7 * BIG, eps=1e-6,
+            inv_lambda=8 * BIG, h_out=3 * BIG, normed=4 * BIG, x_codes=5 * BIG, x_scales=6 * BIG, stream=0)
 
 
 @pytest.mark.parametrize("fn,base,bad", [
@@ -91,7 +91,7 @@ NORM = dict(x_type=0, x=FAKE, ldx=256, residual=2 * BIG, ldr=256, M=64, K=256, n
     ("svdq_gemm_w8a8", GEMM, dict(y_type=3)), ("svdq_gemm_w8a8", GEMM, dict(y_type=-1)),
     ("svdq_quantize_act_w8a8", QUANT, dict(x=None)), ("svdq_quantize_act_w8a8", QUANT, dict(x=FAKE + 2)),
     ("svdq_quantize_act_w8a8", QUANT, dict(x_type=7)), ("svdq_quantize_act_w8a8", QUANT, dict(x_codes=None)),
-    ("svdq_quantize_act_w8a8", QUANT, dict(x_scales=BIG + 4)),
+    ("svdq_quantize_act_w8a8", QUANT, dict(x_scales=2 * BIG + 4)),
     ("svdq_quantize_act_w8a8", QUANT, dict(inv_lambda=FAKE + 4)),
     ("svdq_quantize_act_w8a8", QUANT, dict(x_codes=FAKE + 64 * 512 - 16)),      # codes in x's last row
     ("svdq_pack_weight_w8a8", PACK, dict(W=None)), ("svdq_pack_weight_w8a8", PACK, dict(lam=FAKE)),
@@ -109,6 +109,17 @@ NORM = dict(x_type=0, x=FAKE, ldx=256, residual=2 * BIG, ldr=256, M=64, K=256, n
     ("svdq_rms_norm_quantize_w8a8", NORM, dict(normed=FAKE)), ("svdq_rms_norm_quantize_w8a8", NORM, dict(normed=3 * BIG)),
     ("svdq_rms_norm_quantize_w8a8", NORM, dict(x_codes=2 * BIG)),
     ("svdq_rms_norm_quantize_w8a8", NORM, dict(x_codes=4 * BIG)),
+    ("svdq_rms_norm_quantize_w8a8", NORM, dict(h_out=FAKE + 128, ldx=264, M=1)),   # h in x's row, shifted
+    # scales, y or a weight's side in memory that the call reads or writes otherwise
+    ("svdq_gemm_w8a8", GEMM, dict(y=FAKE)), ("svdq_gemm_w8a8", GEMM, dict(y=FAKE + 64 * 256 - 16)),
+    ("svdq_gemm_w8a8", GEMM, dict(bias=BIG + 64 * 256 * 2 - 16)),
+    ("svdq_quantize_act_w8a8", QUANT, dict(x_scales=FAKE)), ("svdq_quantize_act_w8a8", QUANT, dict(x_scales=BIG + 16)),
+    ("svdq_quantize_act_w8a8", QUANT, dict(inv_lambda=BIG)),
+    ("svdq_pack_weight_w8a8", PACK, dict(w_codes=FAKE)), ("svdq_pack_weight_w8a8", PACK, dict(w_scales=BIG)),
+    ("svdq_pack_weight_w8a8", PACK, dict(lam=FAKE, inv_lambda=FAKE)),
+    ("svdq_rms_norm_quantize_w8a8", NORM, dict(x_scales=4 * BIG)),
+    ("svdq_rms_norm_quantize_w8a8", NORM, dict(x_scales=3 * BIG + 64)),
+    ("svdq_rms_norm_quantize_w8a8", NORM, dict(norm_weight=3 * BIG)),
 ])
 def test_invalid_arguments(L, fn, base, bad):
     assert _status(L, fn, **dict(base, **bad)) == L.SVDQ_ERR_INVALID_ARG
@@ -140,7 +151,7 @@ def test_valid_arguments_reach_the_device_check(L):
                              ("svdq_quantize_act_w8a8", QUANT, dict(ldx=264)),
                              ("svdq_quantize_act_w8a8", QUANT, dict(x_type=2, ldx=260)),
                              ("svdq_pack_weight_w8a8", PACK, {}),
-                             ("svdq_pack_weight_w8a8", PACK, dict(lam=FAKE, inv_lambda=FAKE)),
+                             ("svdq_pack_weight_w8a8", PACK, dict(lam=FAKE, inv_lambda=3 * BIG)),
                              ("svdq_rms_norm_quantize_w8a8", NORM, {}),
                              ("svdq_rms_norm_quantize_w8a8", NORM, dict(h_out=2 * BIG)),
                              ("svdq_rms_norm_quantize_w8a8", NORM, dict(h_out=FAKE)),
