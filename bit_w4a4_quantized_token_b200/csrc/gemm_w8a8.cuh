@@ -29,6 +29,7 @@ struct GemmW8Args {
     int m_tiles, n_tiles;
     int group_m;             // pair kernel: row tiles that are walked together
     int stages;              // narrow kernel: ring depth
+    int tile_n;              // narrow kernel: output channels of a tile (a multiple of 8, at most 128)
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T with signed 8-bit integers, s32 accumulate, on a CTA pair.
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(w8n::kThreads)
     const uint32_t warp = warp_id(), lane = lane_id();
     // the cluster is the whole x extent, a power of two
     const int split = (int)gridDim.x, rank = (int)blockIdx.x, log_split = 31 - __clz(split);
-    const int n0 = (int)blockIdx.y * BN, m0 = (int)blockIdx.z * NT;
+    const int n0 = (int)blockIdx.y * a.tile_n, m0 = (int)blockIdx.z * NT;
     const int c0 = (int)((int64_t)a.chunks * rank / split), c1 = (int)((int64_t)a.chunks * (rank + 1) / split);
 
     if (threadIdx.x == 0) {
@@ -480,7 +481,9 @@ __global__ void __launch_bounds__(w8n::kThreads)
     float sw = 0.0f, bias = 0.0f;
     using T = typename OutType<OUT>::type;
     const int q = (int)(warp & 3u), part = ((int)warp - kEpiWarp0) >> 2;   // an epilogue warp's lane quarter, its turn
-    const int n = n0 + 32 * q + (int)lane;                          // an epilogue thread's output channel
+    // an epilogue thread's output channel; lanes past the tile hold what the
+    // tensor core made of stale shared memory
+    const int n = 32 * q + (int)lane < a.tile_n ? n0 + 32 * q + (int)lane : a.N;
     const int tokens = min(NT, a.M - m0);
     // A stage is kPer chunks of the weight tile, then kPer of the token tile.
     if (warp <= kWarpX) {
@@ -505,7 +508,7 @@ __global__ void __launch_bounds__(w8n::kThreads)
                 } else if (mine) {
                     const int k = kPer == 2 ? (int)warp : 0;   // the chunk of the stage
                     if (c + k < c1) {
-                        mbar_arrive_expect_tx(&full[s], (uint32_t)W_BYTES);
+                        mbar_arrive_expect_tx(&full[s], (uint32_t)(a.tile_n * BK));
                         tma_load_2d(dst + k * W_BYTES, &tm_w, &full[s], (c + k) * BK, n0);
                     } else {
                         mbar_arrive(&full[s]);   // a last stage of one chunk

@@ -905,6 +905,7 @@ svdq_status quantize_rows_w8(svdq_dtype t, const QuantRowsArgs& a, cudaStream_t 
 struct W8Plan {
     bool pair;
     int nt, split, stages;   // narrow kernel: tokens of a tile, CTAs sharing its K range, ring depth
+    int tile_n;              // and its output channels
 };
 // Stages of the narrow kernel's ring: as many as shared memory holds, one when
 // a CTA has no more to do, else an even number, so that each place in the ring
@@ -927,13 +928,21 @@ int w8_ring(int nt, int split, int64_t chunks) {
 // both sides: 256 tokens, N = K = 4096: 64-token tiles 9.7 us, pairs 15.7;
 // 1000 tokens: 128-token tiles 24.6, pairs 16.9; one token, N = K = 4096:
 // split in four 6.5, not split 7.8.
+// Output channels of a narrow tile: as few as `tiles` tiles still cover N with
+// (64 at least), so that every SM of the last wave has its share.  Tiles of 128
+// against these, us: one token, N = 10240, K = 8192 (80 tiles; 143 of 72) 18.6,
+// 16.8; N = 12288, K = 4096 11.9, 11.2; 24 tokens, N = 20480, K = 2560 16.5, 15.6.
+int w8_tile_n(int64_t N, int64_t tiles) {
+    const int64_t rows = round_up((N + tiles - 1) / tiles, 8);
+    return (int)std::clamp<int64_t>(rows, 64, w8n::BN);
+}
 W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t chunks = (K + w8n::BK - 1) / w8n::BK;
     const int64_t weights_ns = N * K / 5700;
     const auto load = [&](int64_t x) { return std::max(x, weights_ns) + std::min(x, weights_ns) / 4; };
     const int sms = num_sms();
     const int mode = g_gemm_tiles_mode.load();
-    W8Plan best = {true, 0, 0, 0};
+    W8Plan best = {true, 0, 0, 0, 0};
     int64_t best_ns = INT64_MAX;
     if (mode != 1) {
         const int64_t tiles = ((M + w8p::BM - 1) / w8p::BM) * ((N + w8p::BN - 1) / w8p::BN);
@@ -958,7 +967,7 @@ W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
             if (l > 0) ns += 1050 + 96 * ((std::min<int64_t>(M, nt) + (1 << l) - 1) >> l);
             if (ns < best_ns) {
                 best_ns = ns;
-                best = {false, nt, 1 << l, w8_ring(nt, 1 << l, chunks)};
+                best = {false, nt, 1 << l, w8_ring(nt, 1 << l, chunks), w8_tile_n(N, std::min<int64_t>(waves * slots[l] / (mt << l), 65535))};
             }
         }
     }
@@ -993,7 +1002,7 @@ svdq_status gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, con
     a.N = (int)N;
     a.chunks = (int)((K + 127) / 128);
     a.last_steps = (int)((K - 128 * (int64_t)(a.chunks - 1) + 31) / 32);
-    const int64_t tm = p.pair ? w8p::BM : p.nt, tn = p.pair ? w8p::BN : w8n::BN;
+    const int64_t tm = p.pair ? w8p::BM : p.nt, tn = p.pair ? w8p::BN : p.tile_n;
     const int64_t mt = (M + tm - 1) / tm, nt = (N + tn - 1) / tn;
     if (p.pair ? mt * nt > (int64_t(1) << 30) : (mt > 65535 || nt > 65535)) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     a.m_tiles = (int)mt;
@@ -1008,8 +1017,10 @@ svdq_status gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, con
     CUtensorMap tm_x, tm_w;
     if (!make_map(&tm_x, CU_TENSOR_MAP_DATA_TYPE_UINT8, x_codes, (uint64_t)K, (uint64_t)M, (uint64_t)K, 128,
                   p.pair ? 128 : (uint32_t)p.nt) ||
-        !make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128, 128))
+        !make_map(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, w_codes, (uint64_t)K, (uint64_t)N, (uint64_t)K, 128,
+                  p.pair ? 128 : (uint32_t)p.tile_n))
         return SVDQ_ERR_CUDA;
+    a.tile_n = p.tile_n;
     if (!p.pair) {
         if (p.nt == 16) return gemm_w8a8_narrow<16>(p, tm_x, tm_w, a, out, st);
         if (p.nt == 32) return gemm_w8a8_narrow<32>(p, tm_x, tm_w, a, out, st);
