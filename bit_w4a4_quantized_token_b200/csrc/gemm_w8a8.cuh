@@ -7,11 +7,31 @@
 // the codes as they lie in memory (K-major rows, 128-byte swizzled TMA boxes)
 // and the epilogue scales once per output.
 //
-// Two kernels compute it:
+// Two kernels compute it, with the same bits (the host picks by an estimate of
+// their times, w8_plan in svdq_lib.cu):
 //  * gemm_w8a8_pair_kernel: 256 x 256 output tiles on two-CTA clusters, for
 //    problems that fill the chip with such tiles;
-//  * gemm_w8a8_narrow_kernel: 128 output channels x 16..256 tokens on single
-//    CTAs with the K range split over a cluster, for few tokens or few tiles.
+//  * gemm_w8a8_narrow_kernel: 64 to 128 output channels x 16 to 128 tokens on
+//    single CTAs, the K range split over a cluster if that pays, for few
+//    tokens or few tiles.
+//
+// Bound.  Many tokens: the tensor pipe.  A pair's stage (two chunks of K, eight
+// M256 N256 K32 MMAs) takes 1030 to 1060 cycles of 1024 at the pipe's 8192
+// products per SM and cycle; ncu: pipe 90 % active at 4608 x 12288 x 4096, its
+// operands read from DRAM once (69 MB).  The board's power cap then sets the
+// clock (1.4 to 1.6 GHz).  Few tokens: the weight's bytes from HBM.  Measured
+// on a B200 (M x N x K, bf16 out, data from HBM, us; P = 10^15 operations a
+// second, 2 M N K; the measured bf16 GEMM peak doubled is 3.26 P, sustained
+// 2.75 P; torch._int_mm, which leaves int32 sums, beside it):
+//     16384 x 8192 x 8192   650-750  2.9-3.4 P   855
+//     4608 x 12288 x 4096   152-169  2.7-3.0 P   207
+//     4608 x 4096 x 12288   147-166  2.8-3.2 P   155
+//     2048 x 6144 x 4096    38       2.7 P       47
+//     1000 x 4104 x 4112    20.6     1.6 P       25   (rows off the 128-byte lines)
+//     16 x 28672 x 8192     41.6     5.7 TB/s         (a plain stream of the weight: 39.9)
+//     1 x 10240 x 8192      16.8     5.0 TB/s
+//     1 x 4096 x 4096       6.6
+//     64 x 256 x 256        2.6      (latency of one tile)
 #pragma once
 #include "gelu_mlp.cuh"        // st_shared_v4
 #include "quantize_w8a8.cuh"   // the element types, pack2
