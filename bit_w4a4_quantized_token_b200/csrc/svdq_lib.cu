@@ -778,10 +778,13 @@ svdq_status check_dims_w8a8(int64_t rows, int64_t K) {
     return SVDQ_OK;
 }
 
+// No matrix of a call has more elements than this, so that byte counts fit in 64 bits.
+constexpr int64_t kW8MaxElements = int64_t(1) << 46;
+
 // A row stride in elements: at least K, and a multiple of 16 bytes.
-svdq_status check_stride(int64_t ld, int64_t K, svdq_dtype t) {
+svdq_status check_stride(int64_t ld, int64_t M, int64_t K, svdq_dtype t) {
     if (ld < K || ld >= (int64_t(1) << 31) || ld * dtype_bytes(t) % 16 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
-    return SVDQ_OK;
+    return M <= kW8MaxElements / ld ? SVDQ_OK : SVDQ_ERR_UNSUPPORTED_SHAPE;
 }
 
 // A range of memory; none when p is null.
@@ -804,14 +807,14 @@ bool any_overlap(std::initializer_list<Span> inputs, std::initializer_list<Span>
     return false;
 }
 
-// Blocks of `threads` threads and `smem` bytes of dynamic shared memory that one SM holds (`slot`: looked up
-// once per device and block size).
-constexpr int kRowThreads = 33;
+// Blocks of `threads` threads that one SM holds by its registers and threads
+// (`slot`: looked up once per device and block size).
+constexpr int kRowThreads = 33;   // block sizes: 32 to 1024 threads in steps of 32
 template <typename Kernel>
-int blocks_per_sm(Kernel kernel, int threads, size_t smem, std::atomic<int>& slot) {
+int blocks_per_sm(Kernel kernel, int threads, std::atomic<int>& slot) {
     int n = slot.load();
     if (n == 0) {
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem) != cudaSuccess || n < 1) {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess || n < 1) {
             cudaGetLastError();
             n = 1;
         }
@@ -835,7 +838,7 @@ svdq_status quantize_rows_held(const QuantRowsArgs& a, cudaStream_t st) {
     const int threads = (int)round_up((a.K / 8 + V - 1) / V, 32);
     const auto kernel = quantize_rows_w8_kernel<T, NORM, V>;
     const int dev = current_device();
-    return launch_rows(kernel, threads, 0, blocks_per_sm(kernel, threads, 0, cache[dev][threads / 32]), a, st);
+    return launch_rows(kernel, threads, 0, blocks_per_sm(kernel, threads, cache[dev][threads / 32]), a, st);
 }
 
 // Of a block's share of an SM's shared memory, what is not rows: barriers, statics, the system's 1 KB.
@@ -858,7 +861,7 @@ svdq_status quantize_rows_ring(const QuantRowsArgs& a, int blocks, cudaStream_t 
     const size_t smem = q8::kRingBarBytes + (size_t)(stages * stage);
     // the blocks that are resident at once share the rows (registers may allow fewer than asked for)
     static std::atomic<int> cache[kMaxDevices][kRowThreads];
-    const int fit = blocks_per_sm(kernel, threads, 0, cache[dev][threads / 32]);
+    const int fit = blocks_per_sm(kernel, threads, cache[dev][threads / 32]);
     return launch_rows(kernel, threads, smem, std::min(blocks, fit), a, st, (int)stages);
 }
 
@@ -891,7 +894,7 @@ svdq_status quantize_rows_typed(const QuantRowsArgs& a, cudaStream_t st) {
     static std::atomic<int> cache[kMaxDevices];
     const auto kernel = quantize_rows_w8_wide_kernel<T, NORM>;
     return launch_rows(kernel, q8::kTwoPassThreads, 0,
-                       blocks_per_sm(kernel, q8::kTwoPassThreads, 0, cache[current_device()]), a, st);
+                       blocks_per_sm(kernel, q8::kTwoPassThreads, cache[current_device()]), a, st);
 }
 
 template <bool NORM>
@@ -917,6 +920,14 @@ int w8_ring(int nt, int split, int64_t chunks) {
     if (most == 1) return 1;
     return (int)(std::min<int64_t>({(int64_t)w8n::kMaxStages, room, most + 1}) / 2 * 2);
 }
+// Output channels of a narrow tile: as few as `tiles` tiles still cover N with
+// (64 at least), so that every SM of the last wave has its share.  Tiles of 128
+// against these, us: one token, N = 10240, K = 8192 (80 tiles; 143 of 72) 18.6,
+// 16.8; N = 12288, K = 4096 11.9, 11.2; 24 tokens, N = 20480, K = 2560 16.5, 15.6.
+int w8_tile_n(int64_t N, int64_t tiles) {
+    const int64_t rows = round_up((N + tiles - 1) / tiles, 8);
+    return (int)std::clamp<int64_t>(rows, 64, w8n::BN);
+}
 // The kernel and tile whose estimated time is least, in nanoseconds:
 //   pair:   5950 + load(waves x 290 per chunk of 128 bytes of K)
 //   narrow: 2650 + load(waves x chunks of a CTA x t) + (split: 1050 + 96 per token that a CTA finishes)
@@ -928,14 +939,6 @@ int w8_ring(int nt, int split, int64_t chunks) {
 // both sides: 256 tokens, N = K = 4096: 64-token tiles 9.7 us, pairs 15.7;
 // 1000 tokens: 128-token tiles 24.6, pairs 16.9; one token, N = K = 4096:
 // split in four 6.5, not split 7.8.
-// Output channels of a narrow tile: as few as `tiles` tiles still cover N with
-// (64 at least), so that every SM of the last wave has its share.  Tiles of 128
-// against these, us: one token, N = 10240, K = 8192 (80 tiles; 143 of 72) 18.6,
-// 16.8; N = 12288, K = 4096 11.9, 11.2; 24 tokens, N = 20480, K = 2560 16.5, 15.6.
-int w8_tile_n(int64_t N, int64_t tiles) {
-    const int64_t rows = round_up((N + tiles - 1) / tiles, 8);
-    return (int)std::clamp<int64_t>(rows, 64, w8n::BN);
-}
 W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
     const int64_t chunks = (K + w8n::BK - 1) / w8n::BK;
     const int64_t weights_ns = N * K / 5700;
@@ -967,7 +970,8 @@ W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
             if (l > 0) ns += 1050 + 96 * ((std::min<int64_t>(M, nt) + (1 << l) - 1) >> l);
             if (ns < best_ns) {
                 best_ns = ns;
-                best = {false, nt, 1 << l, w8_ring(nt, 1 << l, chunks), w8_tile_n(N, std::min<int64_t>(waves * slots[l] / (mt << l), 65535))};
+                const int64_t tiles = std::min<int64_t>(waves * slots[l] / (mt << l), 65535);
+                best = {false, nt, 1 << l, w8_ring(nt, 1 << l, chunks), w8_tile_n(N, tiles)};
             }
         }
     }
@@ -1545,7 +1549,7 @@ svdq_status svdq_quantize_act_w8a8(svdq_dtype x_type, const void* x, int64_t ldx
                                    const float* inv_lambda, void* x_codes, float* x_scales, svdq_stream_t stream) {
     SVDQ_TRY(check_dtype(x_type));
     SVDQ_TRY(check_dims_w8a8(M, K));
-    SVDQ_TRY(check_stride(ldx, K, x_type));
+    SVDQ_TRY(check_stride(ldx, M, K, x_type));
     SVDQ_TRY(check_ptr(x));
     SVDQ_TRY(check_opt_ptr(inv_lambda));
     SVDQ_TRY(check_ptr(x_codes));
@@ -1571,8 +1575,8 @@ svdq_status svdq_rms_norm_quantize_w8a8(svdq_dtype x_type, const void* x, int64_
                                         float* x_scales, svdq_stream_t stream) {
     SVDQ_TRY(check_dtype(x_type));
     SVDQ_TRY(check_dims_w8a8(M, K));
-    SVDQ_TRY(check_stride(ldx, K, x_type));
-    if (residual) SVDQ_TRY(check_stride(ldr, K, x_type));
+    SVDQ_TRY(check_stride(ldx, M, K, x_type));
+    if (residual) SVDQ_TRY(check_stride(ldr, M, K, x_type));
     if (!(eps > 0.0f) || !(eps < 1.0f)) return SVDQ_ERR_INVALID_ARG;
     SVDQ_TRY(check_ptr(x));
     SVDQ_TRY(check_opt_ptr(residual));
@@ -1619,7 +1623,7 @@ svdq_status svdq_gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M
     SVDQ_TRY(check_dtype(y_type));
     SVDQ_TRY(check_dims_w8a8(M, K));
     SVDQ_TRY(check_dims_w8a8(N, K));
-    if (N % 8 != 0) return SVDQ_ERR_UNSUPPORTED_SHAPE;
+    if (N % 8 != 0 || M > kW8MaxElements / N) return SVDQ_ERR_UNSUPPORTED_SHAPE;
     SVDQ_TRY(check_ptr(x_codes));
     SVDQ_TRY(check_ptr(x_scales));
     SVDQ_TRY(check_ptr(w_codes));

@@ -221,6 +221,21 @@ def test_norm_in_place(oracle_mod, where, K):
     assert torch.equal(h, h2) and torch.equal(q.x_codes, q2.x_codes) and torch.equal(q.x_scales, q2.x_scales)
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=str)
+def test_norm_without_residual_copies_the_stream(dtype):
+    """h_out given and no residual: h_out is x; with neither, h is x itself; x as its own h_out."""
+    from bit_w4a4_quantized_token_b200 import layer
+
+    x = draw(33, 1040, dtype, 1).cuda()
+    kept, buf, packed = x.clone(), torch.empty_like(x), packed_for(1040)
+    h1, q1 = layer.rms_norm_quantize_w8a8(x, None, None, packed)
+    h2, q2 = layer.rms_norm_quantize_w8a8(x, None, None, packed, h_out=buf)
+    h3, q3 = layer.rms_norm_quantize_w8a8(x, None, None, packed, h_out=x)
+    assert h1 is x and h2 is buf and h3 is x
+    for h, q in ((h1, q1), (h2, q2), (h3, q3)):
+        assert torch.equal(h, kept) and torch.equal(q.x_codes, q1.x_codes) and torch.equal(q.x_scales, q1.x_scales)
+
+
 def test_norm_special_rows(oracle_mod):
     """A zero row, infinities and NaN, a sum of squares that overflows: no other row changes."""
     from bit_w4a4_quantized_token_b200 import layer
@@ -351,6 +366,22 @@ def test_gemm_writes_its_rows_only_and_nan_rows_stay_alone(M, N, mode):
 
 
 # ------------------------------------------------------- a run of them together
+def test_linear_types_by_default(oracle_mod):
+    """Without a bias y has x's type, with one the bias's, unless it is said; fp32 in and out."""
+    from bit_w4a4_quantized_token_b200 import layer
+
+    W = draw(264, 528, F32, 3)
+    packed = layer.pack_weight_w8a8(W.cuda())
+    with_bias = layer.pack_weight_w8a8(W.cuda(), None, uniform(264, -1.0, 1.0, 1, F16).cuda())
+    for dtype in TYPES:
+        x = draw(50, 528, dtype, 2).cuda()
+        y = layer.w8a8_linear(x, packed)
+        assert y.dtype == dtype and layer.w8a8_linear(x, with_bias).dtype == F16
+        assert layer.w8a8_linear(x, packed, out_dtype=BF16).dtype == BF16
+        codes, scales = oracle_mod.w8a8_quantize_rows(f32(x))
+        check_gemm(torch.from_numpy(codes), torch.from_numpy(scales), packed.w_codes.cpu(), packed.w_scales.cpu(), None, y)
+
+
 def layer_inputs(M, K, N, dtype, smooth):
     x, r = draw(M, K, dtype, 11).cuda(), draw(M, K, dtype, 12, 3.0).cuda()
     W = (torch.randn(N, K, generator=torch.Generator().manual_seed(13)) / K ** 0.5).to(dtype).cuda()

@@ -129,7 +129,8 @@ def test_invalid_arguments(L, fn, base, bad):
     ("svdq_gemm_w8a8", GEMM, dict(M=0)), ("svdq_gemm_w8a8", GEMM, dict(M=1 << 31)),
     ("svdq_gemm_w8a8", GEMM, dict(N=0)), ("svdq_gemm_w8a8", GEMM, dict(N=260)),
     ("svdq_gemm_w8a8", GEMM, dict(K=0)), ("svdq_gemm_w8a8", GEMM, dict(K=24)),
-    ("svdq_gemm_w8a8", GEMM, dict(K=1 << 17)),
+    ("svdq_gemm_w8a8", GEMM, dict(K=1 << 17)), ("svdq_gemm_w8a8", GEMM, dict(M=(1 << 31) - 1, N=(1 << 31) - 8)),
+    ("svdq_quantize_act_w8a8", QUANT, dict(M=(1 << 31) - 1, ldx=(1 << 31) - 8)),
     ("svdq_quantize_act_w8a8", QUANT, dict(M=0)), ("svdq_quantize_act_w8a8", QUANT, dict(K=8)),
     ("svdq_quantize_act_w8a8", QUANT, dict(ldx=255)), ("svdq_quantize_act_w8a8", QUANT, dict(ldx=260)),
     ("svdq_quantize_act_w8a8", QUANT, dict(ldx=0)), ("svdq_quantize_act_w8a8", QUANT, dict(x_type=2, ldx=258)),
