@@ -129,8 +129,6 @@ def svdq_linear(x: torch.Tensor, packed: PackedWeight, x_tensor_scale=None, stre
 _DTYPES = {torch.bfloat16: _lib.SVDQ_BF16, torch.float16: _lib.SVDQ_F16, torch.float32: _lib.SVDQ_F32}
 
 
-
-
 @dataclass(slots=True)
 class PackedWeightW8A8:
     N: int
@@ -174,6 +172,8 @@ def _on_stream(stream, x: torch.Tensor, fn, *args):
     """fn(*args) with `stream` (a torch stream or a raw handle) current, so that what it allocates is ordered with
     that stream's work.  The tensors it reads are marked as in use there, those it returns as in use on the caller's
     stream, so that the allocator hands out no memory early; the two streams' order is the caller's to keep."""
+    if not isinstance(stream, int) and stream.device != x.device:
+        raise ValueError(f"stream: expected a stream of {x.device}, where the operands are, got one of {stream.device}")
     caller = torch.cuda.current_stream(x.device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)

@@ -191,3 +191,22 @@ def test_layer_refuses_what_a_pointer_hides(L):
         layer.gemm_w8a8(q, packed, y=torch.zeros(8, 16))
     with pytest.raises(ValueError, match="W:"):
         layer.pack_weight_w8a8(torch.zeros(8, 32))
+
+
+def test_stream_of_another_device_is_refused(L):
+    """A stream belongs to one GPU: work for an operand elsewhere would run on that operand's current stream."""
+    from types import SimpleNamespace
+
+    from bit_w4a4_quantized_token_b200 import layer
+
+    other = SimpleNamespace(device=torch.device("cuda", 1))
+    codes, scales = torch.zeros(8, 32, dtype=torch.int8), torch.zeros(8)
+    packed = layer.PackedWeightW8A8(8, 32, codes, scales, None, None)
+    x = torch.zeros(4, 32, dtype=torch.bfloat16)
+    for call in (lambda: layer.quantize_act_w8a8(x, packed, stream=other),
+                 lambda: layer.rms_norm_quantize_w8a8(x, None, None, packed, stream=other),
+                 lambda: layer.gemm_w8a8(layer.QuantizedActW8A8(8, codes, scales), packed, stream=other),
+                 lambda: layer.w8a8_linear(x, packed, stream=other),
+                 lambda: layer.pack_weight_w8a8(torch.zeros(8, 32), stream=other)):
+        with pytest.raises(ValueError, match="stream:"):
+            call()
