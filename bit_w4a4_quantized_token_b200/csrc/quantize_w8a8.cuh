@@ -15,7 +15,7 @@
 //   * a < 2^-100 (127 / a near the end of fp32): codes and scale 0.
 //   * a row that holds an infinity or a NaN, or whose sum of squares
 //     overflows fp32: codes 0 and scale NaN, so that the whole output row,
-//     and no other, is NaN.  The maximum is taken over the bit patterns of
+//     and no other, is NaN, and the whole normalised row too.  The maximum is taken over the bit patterns of
 //     |t| as unsigned integers, where NaN > infinity > every finite value.
 //
 // Bound: memory traffic.  Per element b read (2 b with a residual), 1 byte of
@@ -180,9 +180,12 @@ __device__ __forceinline__ RowFactors row_factors(uint32_t abits, float ss, int 
     f.rstd = 1.0f;
     bool bad = abits >= 0x7F800000u;
     if (NORM) {
-        f.rstd = __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)K), eps));
+        // an infinite sum has the factor NaN, not the 0 that its root gives:
+        // the normalised values of a finite row would be zeros
+        const bool lost = !(ss < __int_as_float(0x7F800000));
+        f.rstd = lost ? __int_as_float(0x7FC00000) : __frsqrt_rn(__fadd_rn(__fdiv_rn(ss, (float)K), eps));
         f.scale = __fmul_rn(f.scale, f.rstd);
-        bad = bad || !(ss < __int_as_float(0x7F800000));
+        bad = bad || lost;
     }
     if (bad) {
         f.inv = 0.0f;

@@ -366,7 +366,7 @@ svdq_status svdq_gemm_w4a16(const void* x, int64_t M, const void* w_codes, const
  * in fp32, each step rounded once.  A row with a < 2^-100 gets codes and scale
  * 0.  A row that holds an infinity or a NaN (or, with the norm, whose sum of
  * squares overflows fp32) gets codes 0 and scale NaN: its whole row of y, and
- * no other, is NaN.
+ * no other, is NaN; so is its whole row of the norm's `normed`.
  * Layouts: codes [rows, K] int8, row-major; scales [rows] fp32; K needs no
  * padding.  Sizes: 1 <= rows < 2^31; 16 <= K < 2^17, K % 16 == 0 (the int32
  * sum cannot overflow, whatever the codes); N % 8 == 0.

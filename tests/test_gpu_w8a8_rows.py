@@ -101,3 +101,22 @@ def test_norm_special_rows_among_many(oracle_mod, dtype, M, K):
     rest = [m for m in range(M) if m not in rows]
     q.x_codes, q.x_scales = q.x_codes[rest], q.x_scales[rest]
     check_norm(oracle_mod, q, x[rest], r[rest], w, None)
+
+
+@pytest.mark.parametrize("dtype,M,K", [(BF16, 300, 272), (BF16, 700, 8192), (F32, 40, 512), (F32, 700, 4112),
+                                       (BF16, 40, 32768)])
+def test_normed_of_rows_without_a_finite_sum(dtype, M, K):
+    """A NaN, an infinity or finite values whose squares overflow: the whole normalised row is NaN (never zeros), and
+    no other row changes."""
+    from bit_w4a4_quantized_token_b200 import layer
+
+    x, r = draw(M, K, dtype, 8), draw(M, K, dtype, 9)
+    x[3, 5], x[M - 2, K - 1], r[M // 2, 0] = float("nan"), 1e30, float("-inf")
+    bad = [3, M // 2, M - 2]
+    rest = [m for m in range(M) if m not in bad]
+    w, packed = uniform(K, 0.5, 2.0, 7, dtype).cuda(), packed_for(K)
+    normed, alone = (torch.empty(n, K, dtype=dtype, device="cuda") for n in (M, M - 3))
+    _, q = layer.rms_norm_quantize_w8a8(x.cuda(), r.cuda(), w, packed, normed=normed)
+    layer.rms_norm_quantize_w8a8(x[rest].cuda(), r[rest].cuda(), w, packed, normed=alone)
+    assert bool(torch.isnan(q.x_scales[bad]).all()) and bool(torch.isnan(normed[bad]).all())
+    assert bool(torch.isfinite(alone).all()) and torch.equal(normed[rest], alone)
