@@ -14,7 +14,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _ROOT = os.path.dirname(_HERE)
 LIB = os.path.join(_HERE, "libsvdq_b200.so")
 SOURCES = sorted(glob.glob(os.path.join(_HERE, "csrc", "*.cu")) + glob.glob(os.path.join(_HERE, "csrc", "*.cuh"))
-                 + [os.path.join(_ROOT, "include", "svdq.h")])
+                 + glob.glob(os.path.join(_HERE, "csrc", "*.h")) + [os.path.join(_ROOT, "include", "svdq.h")])
 MAIN = os.path.join(_HERE, "csrc", "svdq_lib.cu")
 FRONT = os.path.join(_HERE, "_w8a8_front.so")
 FRONT_MAIN = os.path.join(_HERE, "csrc", "w8a8_front.cpp")

@@ -35,6 +35,7 @@
 // 16384, K = 8192 74 us (0.82); one token, K = 8192 2.6 us, all latency.
 #pragma once
 #include "sm100_ptx.cuh"
+#include "w8a8_plan.h"
 
 namespace svdq {
 
@@ -405,10 +406,10 @@ __global__ void __launch_bounds__(q8::kRingThreads) quantize_rows_w8_ring_kernel
     }
     int s = 0, buf = 0;
     uint32_t ph = 0u;
-    bool alive = true;
+    int lost = -1;   // the row whose wait ran out
     for (int row = (int)blockIdx.x; row < a.M; row = next_row(row, a.M), buf ^= 1) {
         // after a timeout the block runs on without waiting and without fetching (its rows are void)
-        if (alive) alive = bounded_wait(&full[s], ph, kSiteQ8Full);
+        if (lost < 0 && !bounded_wait(&full[s], ph, kSiteQ8Full)) lost = row;
         const uint8_t* src = rows + (size_t)s * stage_bytes;
         float h[V][8];
         uint32_t abits = 0u;
@@ -437,7 +438,7 @@ __global__ void __launch_bounds__(q8::kRingThreads) quantize_rows_w8_ring_kernel
             }
         }
         group_reduce<NORM>(abits, ss, slots[buf], (int)warp_id(), step);
-        if (tid == 0 && alive && ahead < a.M) {
+        if (tid == 0 && lost < 0 && ahead < a.M) {
             fetch(ahead, s);
             ahead = next_row(ahead, a.M);
         }
@@ -456,10 +457,10 @@ __global__ void __launch_bounds__(q8::kRingThreads) quantize_rows_w8_ring_kernel
             }
         }
     }
-    // no copy is in flight when the block ends, even after a timeout: the
-    // stages from s on were fetched and not waited for (best effort, bounded)
-    if (tid == 0 && !alive)
-        for (int i = 0; i < stages; ++i) mbar_wait(&full[i], 0u, kSiteQ8Drain);
+    // no copy is in flight when the block ends, even after a timeout (best effort: each wait is bounded)
+    if (tid == 0 && lost >= 0)
+        drain_ring((int)blockIdx.x, (int)gridDim.x, lost, ahead, stages,
+                   [&](int i, uint32_t parity) { mbar_wait(&full[i], parity, kSiteQ8Drain); });
 }
 
 // Rows too wide for the registers of one block: statistics in a first pass

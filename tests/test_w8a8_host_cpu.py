@@ -1,0 +1,70 @@
+"""Arithmetic of the W8A8 kernels and their launches, compiled alone for the
+host (csrc/w8a8_plan.h) and checked over its whole range."""
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_w4a4_quantized_token_b200", "csrc")
+
+
+@pytest.fixture(scope="module")
+def run(tmp_path_factory):
+    """Compiles and runs a C++ program beside the header; returns what it prints."""
+    where = tmp_path_factory.mktemp("w8a8")
+
+    def compiled(body):
+        src, exe = where / "main.cpp", where / "main"
+        src.write_text('#include "w8a8_plan.h"\n#include <cstdio>\n#include <vector>\nusing namespace svdq;\n' + body)
+        subprocess.check_call([os.environ.get("CXX", "g++"), "-O1", "-std=c++17", "-Wall", "-Werror", "-I", CSRC, "-o",
+                               str(exe), str(src)])
+        return subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=120).stdout
+
+    return compiled
+
+
+DRAIN = """
+// The ring as the kernel runs it, one barrier per place that counts its finished phases, up to the row whose wait
+// runs out: its copy and the later ones are in flight then.
+int main() {
+    long cases = 0, bad = 0;
+    for (int stages = 2; stages <= 8; ++stages)
+        for (int step = 1; step <= 148; step += 49)
+            for (int first = 0; first < step; first += 16)
+                for (int M = first + 1; M < first + 40 * step; M += 1 + step / 3)
+                    for (int fail = 0; first + fail * step < M; ++fail) {
+                        std::vector<int> done(stages, 0), fill(stages, -1);   // finished phases; copy in flight
+                        int ahead = first, n = 0;
+                        const auto fetch = [&](int s) {
+                            fill[s] = n++;
+                            ahead = ahead + (long)step < M ? ahead + step : M;
+                        };
+                        for (int s = 0; s < stages && ahead < M; ++s) fetch(s);
+                        int s = 0;
+                        for (int i = 0; i < fail; ++i, s = (s + 1) % stages) {
+                            ++done[s], fill[s] = -1;                          // row i has landed and is read
+                            if (ahead < M) fetch(s);
+                        }
+                        std::vector<int> waits(stages, 0);
+                        drain_ring(first, step, first + fail * step, ahead, stages, [&](int place, unsigned parity) {
+                            ++waits[place];
+                            // a wait for the phase that is under way, and not one that returns at once
+                            if (fill[place] < 0 || parity != (unsigned)(done[place] & 1)) ++bad;
+                        });
+                        for (int p = 0; p < stages; ++p) bad += waits[p] != (fill[p] >= 0);
+                        ++cases;
+                    }
+    const int big = 2147483647;   // the largest number of rows
+    int waits = 0;
+    drain_ring(147, 148, 147 + 148 * 14510000, big, 8, [&](int, unsigned) { ++waits; });
+    std::printf("%ld cases, %ld bad, %d\\n", cases, bad, waits);
+}
+"""
+
+
+def test_drain_waits_for_the_copies_in_flight_and_no_others(run):
+    """After a timeout at any row of any ring: one wait for each copy in flight, in its own phase."""
+    out = run(DRAIN).split()
+    assert int(out[0]) > 50000 and out[2] == "0", out
+    rows = -(-(2147483647 - 147) // 148)
+    assert int(out[4]) == rows - 14510000
