@@ -71,15 +71,15 @@ __device__ __forceinline__ float bias_at(const void* bias, int out, int n) {
 }
 
 enum : uint32_t {
-    kSiteW8Empty = 40,
-    kSiteW8Full = 41,
-    kSiteW8Acc = 42,
-    kSiteW8AccEmpty = 43,
-    kSiteW8Drain = 44,
-    kSiteW8NarrowEmpty = 45,
-    kSiteW8NarrowFull = 46,
-    kSiteW8NarrowAcc = 47,
-    kSiteW8NarrowDrain = 48
+    kSiteW8Empty = 56,
+    kSiteW8Full = 57,
+    kSiteW8Acc = 58,
+    kSiteW8AccEmpty = 59,
+    kSiteW8Drain = 60,
+    kSiteW8NarrowEmpty = 61,
+    kSiteW8NarrowFull = 62,
+    kSiteW8NarrowAcc = 63,
+    kSiteW8NarrowDrain = 64
 };
 
 // ------------------------------------------------------------ CTA-pair kernel

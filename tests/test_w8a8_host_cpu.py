@@ -1,6 +1,8 @@
 """Arithmetic of the W8A8 kernels and their launches, compiled alone for the
 host (csrc/w8a8_plan.h) and checked over its whole range."""
+import glob
 import os
+import re
 import subprocess
 
 import pytest
@@ -68,3 +70,13 @@ def test_drain_waits_for_the_copies_in_flight_and_no_others(run):
     assert int(out[0]) > 50000 and out[2] == "0", out
     rows = -(-(2147483647 - 147) // 148)
     assert int(out[4]) == rows - 14510000
+
+
+def test_every_wait_site_has_a_number_of_its_own():
+    """The device status word names a wait by one byte: two kernels with the same number could not be told apart."""
+    sites = {}
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        for name, number in re.findall(r"\b(kSite\w+) = (\d+)", open(path).read()):
+            sites.setdefault(int(number), set()).add(name)
+    assert len(sites) > 30 and all(0 < n < 256 for n in sites)
+    assert all(len(names) == 1 for names in sites.values()), {n: s for n, s in sites.items() if len(s) > 1}
