@@ -19,7 +19,7 @@ from dataclasses import dataclass, fields
 
 import torch
 
-from . import _lib, _w8a8_front as _front
+from . import _lib
 
 _U8 = torch.uint8
 
@@ -150,11 +150,27 @@ def _raise_status(status: int, name: str) -> None:
     raise _lib.SvdqError(status, name)
 
 
+class _Unloaded:
+    """Stands for the native module of the W8A8 functions until one of them is called: what does not use it, the 4-bit
+    layer, does not need it."""
+
+    def __getattr__(self, name):
+        global _front
+        try:
+            from . import _w8a8_front as module
+        except ImportError as e:
+            raise ImportError("the native module of the W8A8 layer is not built for this Python and torch; run "
+                              "__graft_entry__.build() (there is no fallback)") from e
+        module.bind(*(ctypes.cast(getattr(_lib.lib, fn), ctypes.c_void_p).value
+                      for fn in ("svdq_pack_weight_w8a8", "svdq_quantize_act_w8a8", "svdq_rms_norm_quantize_w8a8",
+                                 "svdq_gemm_w8a8")), _raise_status)
+        _front = module
+        return getattr(module, name)
+
+
 # The operands' checks, the outputs' allocation and the library call are one call of a small native module: a layer
 # call on few tokens is bound by what the host does for it, and in Python that was twice the GPU's time.
-_front.bind(*(ctypes.cast(getattr(_lib.lib, name), ctypes.c_void_p).value
-              for name in ("svdq_pack_weight_w8a8", "svdq_quantize_act_w8a8", "svdq_rms_norm_quantize_w8a8",
-                           "svdq_gemm_w8a8")), _raise_status)
+_front = _Unloaded()
 
 
 def _tensors(v):

@@ -1,0 +1,55 @@
+"""The W8A8 layer's native module: what needs it, what does not, and when it is built anew."""
+import os
+import shutil
+import subprocess
+import sys
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+PACKAGE = "bit_w4a4_quantized_token_b200"
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from bit_w4a4_quantized_token_b200 import build
+
+    build.build()
+
+
+def copy_without_module(where):
+    """The package as built, but for the native module."""
+    shutil.copytree(os.path.join(ROOT, PACKAGE), os.path.join(where, PACKAGE),
+                    ignore=shutil.ignore_patterns("_w8a8_front*", "csrc", "__pycache__"))
+
+
+def python(code, where):
+    return subprocess.run([sys.executable, "-c", code], cwd=where, capture_output=True, text=True, timeout=300,
+                          env=dict(os.environ, PYTHONPATH=str(where)))
+
+
+WITHOUT = """
+import torch
+from bit_w4a4_quantized_token_b200 import layer
+assert callable(layer.svdq_linear) and callable(layer.pack_weight)
+packed = layer.PackedWeightW8A8(8, 32, torch.zeros(8, 32, dtype=torch.int8), torch.zeros(8), None, None)
+x = torch.zeros(4, 32, dtype=torch.bfloat16)
+q = layer.QuantizedActW8A8(8, packed.w_codes, packed.w_scales)
+for call in (lambda: layer.pack_weight_w8a8(torch.zeros(8, 32)), lambda: layer.quantize_act_w8a8(x, packed),
+             lambda: layer.rms_norm_quantize_w8a8(x, None, None, packed), lambda: layer.gemm_w8a8(q, packed),
+             lambda: layer.w8a8_linear(x, packed)):
+    try:
+        call()
+    except ImportError as e:
+        assert "not built" in str(e), e
+    else:
+        raise AssertionError("a W8A8 function ran without its native module")
+print("as it should be")
+"""
+
+
+def test_the_4_bit_layer_does_not_need_the_module(tmp_path):
+    """Without it the package imports, and the W8A8 functions say what is missing when they are called."""
+    copy_without_module(tmp_path)
+    r = python(WITHOUT, tmp_path)
+    assert r.returncode == 0 and "as it should be" in r.stdout, r.stderr[-2000:]
