@@ -55,9 +55,28 @@ def _compile(out: str, sources: list[str], command, force: bool, verbose: bool) 
     return out
 
 
+def front_lacks() -> str:
+    """What the native module needs and this machine does not have ("" when it has all)."""
+    import importlib.util
+    import sysconfig
+
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return "torch"
+    if not os.path.exists(os.path.join(spec.submodule_search_locations[0], "lib", "libc10_cuda.so")):
+        return "a torch with CUDA"
+    return "" if os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")) else "Python's headers"
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    _compile(FRONT, [FRONT_MAIN, os.path.join(_ROOT, "include", "svdq.h")], front_command, force, verbose)
-    return _compile(LIB, SOURCES, nvcc_command, force, verbose)
+    """The library first: it needs no more than nvcc, and neither do the C ABI's users."""
+    lib = _compile(LIB, SOURCES, nvcc_command, force, verbose)
+    lacking = front_lacks()
+    if lacking:
+        print(f"the W8A8 layer's Python module is not built: no {lacking}", file=sys.stderr)
+    else:
+        _compile(FRONT, [FRONT_MAIN, os.path.join(_ROOT, "include", "svdq.h")], front_command, force, verbose)
+    return lib
 
 
 if __name__ == "__main__":

@@ -53,3 +53,25 @@ def test_the_4_bit_layer_does_not_need_the_module(tmp_path):
     copy_without_module(tmp_path)
     r = python(WITHOUT, tmp_path)
     assert r.returncode == 0 and "as it should be" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("lacking", [None, "torch", "a torch with CUDA", "Python's headers"])
+def test_the_library_is_built_without_what_the_module_needs(monkeypatch, capsys, tmp_path, lacking):
+    """The library comes first, whatever the machine lacks for the module, and what is not built is said."""
+    import sysconfig
+
+    from bit_w4a4_quantized_token_b200 import build
+
+    outputs = []
+    monkeypatch.setattr(build, "_compile", lambda out, *rest: outputs.append(os.path.basename(out)) or out)
+    if lacking == "torch":
+        monkeypatch.setitem(sys.modules, "torch", None)
+    elif lacking == "a torch with CUDA":
+        exists = os.path.exists
+        monkeypatch.setattr(os.path, "exists", lambda p: not str(p).endswith("libc10_cuda.so") and exists(p))
+    elif lacking:
+        monkeypatch.setattr(sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert build.build() == build.LIB
+    assert outputs[0] == "libsvdq_b200.so" and len(outputs) == (1 if lacking else 2)
+    err = capsys.readouterr().err
+    assert (f"not built: no {lacking}" in err) if lacking else err == ""
