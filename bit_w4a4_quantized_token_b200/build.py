@@ -1,5 +1,6 @@
 """Compile the CUDA library (sm_100a) in-tree, libsvdq_b200.so next to this file,
-and the CPython module beside it that makes the W8A8 layer's calls (_w8a8_front.so).
+and the CPython module beside it that makes the W8A8 layer's calls (_w8a8_front.<torch and
+Python it was built for>.so).
 
     python -m bit_w4a4_quantized_token_b200.build [--force]
 """
@@ -16,7 +17,6 @@ LIB = os.path.join(_HERE, "libsvdq_b200.so")
 SOURCES = sorted(glob.glob(os.path.join(_HERE, "csrc", "*.cu")) + glob.glob(os.path.join(_HERE, "csrc", "*.cuh"))
                  + glob.glob(os.path.join(_HERE, "csrc", "*.h")) + [os.path.join(_ROOT, "include", "svdq.h")])
 MAIN = os.path.join(_HERE, "csrc", "svdq_lib.cu")
-FRONT = os.path.join(_HERE, "_w8a8_front.so")
 FRONT_MAIN = os.path.join(_HERE, "csrc", "w8a8_front.cpp")
 
 
@@ -26,7 +26,17 @@ def nvcc_command(out: str = LIB) -> list[str]:
             "-Xcompiler", "-fPIC", "-shared", "-I" + os.path.join(_ROOT, "include"), "-o", out, MAIN]
 
 
-def front_command(out: str = FRONT) -> list[str]:
+def front_path() -> str:
+    """The native module's file for the running Python and torch: its name holds both, because it is compiled against
+    the C++ of the one and the C API of the other and is of no use to any other pair."""
+    import sysconfig
+
+    import torch
+
+    return os.path.join(_HERE, f"_w8a8_front.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def front_command(out: str) -> list[str]:
     import sysconfig
 
     import torch
@@ -75,7 +85,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if lacking:
         print(f"the W8A8 layer's Python module is not built: no {lacking}", file=sys.stderr)
     else:
-        _compile(FRONT, [FRONT_MAIN, os.path.join(_ROOT, "include", "svdq.h")], front_command, force, verbose)
+        _compile(front_path(), [FRONT_MAIN, os.path.join(_ROOT, "include", "svdq.h")], front_command, force, verbose)
     return lib
 
 

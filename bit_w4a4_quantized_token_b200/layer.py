@@ -15,11 +15,13 @@ The 8-bit integer (W8A8) layer, for the layers that 4 bits cost too much:
 from __future__ import annotations
 
 import ctypes
+import importlib.util
+import os
 from dataclasses import dataclass, fields
 
 import torch
 
-from . import _lib
+from . import _lib, build
 
 _U8 = torch.uint8
 
@@ -156,11 +158,13 @@ class _Unloaded:
 
     def __getattr__(self, name):
         global _front
-        try:
-            from . import _w8a8_front as module
-        except ImportError as e:
-            raise ImportError("the native module of the W8A8 layer is not built for this Python and torch; run "
-                              "__graft_entry__.build() (there is no fallback)") from e
+        path = build.front_path()
+        if not os.path.exists(path):
+            raise ImportError(f"the native module of the W8A8 layer is not built for this Python and torch ({path}); "
+                              "run __graft_entry__.build() (there is no fallback)")
+        spec = importlib.util.spec_from_file_location(f"{__package__}._w8a8_front", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
         module.bind(*(ctypes.cast(getattr(_lib.lib, fn), ctypes.c_void_p).value
                       for fn in ("svdq_pack_weight_w8a8", "svdq_quantize_act_w8a8", "svdq_rms_norm_quantize_w8a8",
                                  "svdq_gemm_w8a8")), _raise_status)

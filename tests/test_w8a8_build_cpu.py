@@ -75,3 +75,32 @@ def test_the_library_is_built_without_what_the_module_needs(monkeypatch, capsys,
     assert outputs[0] == "libsvdq_b200.so" and len(outputs) == (1 if lacking else 2)
     err = capsys.readouterr().err
     assert (f"not built: no {lacking}" in err) if lacking else err == ""
+
+
+def test_a_module_of_another_torch_or_python_is_not_used(monkeypatch):
+    """After an upgrade of either the old file is neither loaded nor taken as built."""
+    import sysconfig
+
+    import torch
+
+    from bit_w4a4_quantized_token_b200 import build, layer
+
+    here, config = build.front_path(), sysconfig.get_config_var
+    outputs = []
+    monkeypatch.setattr(build, "_compile", lambda out, *rest: outputs.append(out) or out)
+    monkeypatch.setattr(layer, "_front", layer._Unloaded())
+    for change in ("torch", "python"):
+        with monkeypatch.context() as m:
+            if change == "torch":
+                m.setattr(torch, "__version__", "99.0.0")
+            else:
+                m.setattr(sysconfig, "get_config_var", lambda name: ".cpython-399-x86_64-linux-gnu.so"
+                          if name == "EXT_SUFFIX" else config(name))
+            build.build()
+            assert outputs[-1] != here and not os.path.exists(outputs[-1])
+            with pytest.raises(ImportError, match="not built"):
+                layer.quantize_act_w8a8(torch.zeros(4, 32), layer.PackedWeightW8A8(8, 32, None, None, None, None))
+    build.build()
+    assert outputs[-1] == here
+    with pytest.raises(ValueError, match="x:"):
+        layer.quantize_act_w8a8(torch.zeros(4, 32), layer.PackedWeightW8A8(8, 32, None, None, None, None))
