@@ -869,9 +869,10 @@ svdq_status quantize_rows_ring(const QuantRowsArgs& a, int blocks, cudaStream_t 
 //   * the ring where a row's bytes (x and residual) reach 16 KB and two rows
 //     fit: norm, M = 4608: K = 4096 24.2 (held 25.7), K = 2048 14.1 (13.9);
 //     norm, M = 16384, K = 8192 160 (held 223); quantise, M = 4608, K = 12288
-//     35.0 (42.6), K = 4096 13.2 (12.6).  Two blocks per SM when they can each
-//     hold two rows, but one, with all the memory, for rows of 32 KB in large
-//     numbers (M = 16384, K = 8192: 160 against 170; M = 600: 11.0 against 9.4).
+//     35.0 (42.6), K = 4096 13.2 (12.6).  Two blocks per SM (four of half
+//     the threads up to 4096 columns) when they can each hold two rows, but
+//     one, with all the memory, for rows of 32 KB in large numbers (M = 16384,
+//     K = 8192: 160 against 170; M = 600: 11.0 against 9.4).
 //     fp32 norms of up to 4096 columns stay in registers all the same (M =
 //     16384, K = 4096: 148 against 154; M = 512: 6.8 against 8.8).
 //   * else in registers: one vector of eight per thread with a norm (M = 4608,
@@ -890,7 +891,8 @@ svdq_status quantize_rows_typed(const QuantRowsArgs& a, cudaStream_t st) {
         return quantize_rows_ring<T, NORM>(a, blocks, st);
     }
     if (nvec <= (NORM ? q8::kMaxThreads : 128)) return quantize_rows_held<T, NORM, 1>(a, st);
-    if (nvec <= 2 * q8::kMaxThreads) return quantize_rows_held<T, NORM, 2>(a, st);
+    if constexpr (!(T == kF32 && NORM))   // such rows of 513 vectors are 16 KB: the ring's
+        if (nvec <= 2 * q8::kMaxThreads) return quantize_rows_held<T, NORM, 2>(a, st);
     static std::atomic<int> cache[kMaxDevices];
     const auto kernel = quantize_rows_w8_wide_kernel<T, NORM>;
     return launch_rows(kernel, q8::kTwoPassThreads, 0,

@@ -104,3 +104,15 @@ def test_a_module_of_another_torch_or_python_is_not_used(monkeypatch):
     assert outputs[-1] == here
     with pytest.raises(ValueError, match="x:"):
         layer.quantize_act_w8a8(torch.zeros(4, 32), layer.PackedWeightW8A8(8, 32, None, None, None, None))
+
+
+def test_no_row_kernel_that_no_call_reaches():
+    """The fp32 norm holds at most one vector of eight a thread in registers: wider rows are 16 KB, the ring's."""
+    import re
+
+    from bit_w4a4_quantized_token_b200 import build
+
+    names = subprocess.check_output(["nm", build.LIB], text=True)
+    held = {tuple(map(int, m)) for m in re.findall(r"quantize_rows_w8_kernelILi(\d)ELb(\d)ELi(\d)E", names)}
+    bf16, f16, f32 = range(3)
+    assert held == {(t, norm, v) for t in (bf16, f16, f32) for norm in (0, 1) for v in (1, 2)} - {(f32, 1, 2)}
