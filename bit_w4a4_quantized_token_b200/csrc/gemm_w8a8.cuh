@@ -8,7 +8,7 @@
 // and the epilogue scales once per output.
 //
 // Two kernels compute it, with the same bits (the host picks by an estimate of
-// their times, w8_plan in svdq_lib.cu):
+// their times, w8_plan in w8a8_plan.h):
 //  * gemm_w8a8_pair_kernel: 256 x 256 output tiles on two-CTA clusters, for
 //    problems that fill the chip with such tiles;
 //  * gemm_w8a8_narrow_kernel: 64 to 128 output channels x 16 to 128 tokens on
@@ -35,6 +35,7 @@
 #pragma once
 #include "gelu_mlp.cuh"        // st_shared_v4
 #include "quantize_w8a8.cuh"   // the element types, pack2
+#include "w8a8_plan.h"         // tile sizes, shared memory of the narrow kernel
 
 namespace svdq {
 
@@ -84,9 +85,6 @@ enum : uint32_t {
 
 // ------------------------------------------------------------ CTA-pair kernel
 namespace w8p {
-constexpr int BM = 256;                       // tokens of a tile (128 per CTA)
-constexpr int BN = 256;                       // output channels of a tile (128 weight rows loaded per CTA)
-constexpr int BK = 128;                       // bytes of K of a chunk: the rows of a swizzled box
 constexpr int kPer = 2;                       // chunks per stage
 constexpr int kStages = 3;
 constexpr int A_BYTES = 128 * BK;             // of one chunk
@@ -372,15 +370,6 @@ __global__ void __launch_bounds__(w8p::kThreads, 1)
 
 // -------------------------------------------------------------- narrow kernel
 namespace w8n {
-constexpr int BN = 128;                       // output channels of a tile: the MMA's M
-constexpr int BK = 128;
-// Chunks of K per stage: two where the tokens add little to a stage's bytes
-// (one barrier round trip for both), one where two would leave the ring with
-// two stages.
-__host__ __device__ constexpr int per(int nt) { return nt <= 64 ? 2 : 1; }
-constexpr int W_BYTES = BN * BK;              // of one chunk
-constexpr int kMaxStages = 8;
-constexpr int kMaxSplit = 8;                  // CTAs of a cluster that share a tile's K range
 constexpr int kEpiWarps = 8;                  // two per TMEM lane quarter, taking turns of 16 tokens
 // A thread issues a TMA load about every 300 cycles whatever the size of its
 // box, so three share the loads: two take turns with the weight boxes, one
@@ -392,18 +381,7 @@ constexpr int kWarpW0 = 0, kWarpW1 = 1, kWarpX = 2;
 // weights a cycle.
 constexpr int kWarpMma0 = 3, kWarpMma1 = 4, kEpiWarp0 = 5;
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
-constexpr int kBarBytes = 512;
 static_assert((2 * kMaxStages + 1) * 8 + 4 <= kBarBytes, "barriers do not fit");
-__host__ __device__ constexpr int stage_bytes(int nt) { return per(nt) * (W_BYTES + nt * BK); }
-// int32 partial sums that a CTA receives: for each of its tokens (every
-// split-th of the tile) 128 channels from every CTA of the cluster
-__host__ __device__ constexpr int partial_bytes(int nt, int split) {
-    return split == 1 ? 0 : (nt + split - 1) / split * split * BN * 4;
-}
-// alignment slack, barriers, token scales, partial sums
-__host__ __device__ constexpr int fixed_bytes(int nt, int split) {
-    return 1024 + kBarBytes + nt * 4 + partial_bytes(nt, split);
-}
 }  // namespace w8n
 
 __device__ __forceinline__ uint32_t cluster_addr_u32(uint32_t addr, uint32_t rank) {

@@ -62,6 +62,7 @@ svdq_status check_opt_ptr(const void* p) { return (p == nullptr || aligned16(p))
         if (_st != SVDQ_OK) return _st;         \
     } while (0)
 
+
 int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
 // ------------------------------------------------------------ the device
@@ -75,8 +76,6 @@ bool g_device_ready[kMaxDevices];
 // Budget of dynamic shared memory for the activation quantizer (the opt-in
 // maximum is 227 KB per block including static shared memory).
 constexpr int kQuantSmemBudget = 226 * 1024;
-// The same for the ring buffers of the W8A8 kernels, with room for their static shared memory.
-constexpr int kW8SmemBudget = 224 * 1024;
 
 thread_local char g_last_error[256] = "";
 
@@ -906,78 +905,37 @@ svdq_status quantize_rows_w8(svdq_dtype t, const QuantRowsArgs& a, cudaStream_t 
     return quantize_rows_typed<kBf16, NORM>(a, st);
 }
 
-// How svdq_gemm_w8a8 runs a shape.
-struct W8Plan {
-    bool pair;
-    int nt, split, stages;   // narrow kernel: tokens of a tile, CTAs sharing its K range, ring depth
-    int tile_n;              // and its output channels
-};
-// Stages of the narrow kernel's ring: as many as shared memory holds, one when
-// a CTA has no more to do, else an even number, so that each place in the ring
-// belongs to one of the two MMA warps (a warp must see every phase of a
-// barrier that it waits on: parities repeat).
-int w8_ring(int nt, int split, int64_t chunks) {
-    const int64_t most = ((chunks + split - 1) / split + w8n::per(nt) - 1) / w8n::per(nt);
-    const int64_t room = (kW8SmemBudget - w8n::fixed_bytes(nt, split)) / w8n::stage_bytes(nt);
-    if (most == 1) return 1;
-    return (int)(std::min<int64_t>({(int64_t)w8n::kMaxStages, room, most + 1}) / 2 * 2);
-}
-// Output channels of a narrow tile: as few as `tiles` tiles still cover N with
-// (64 at least), so that every SM of the last wave has its share.  Tiles of 128
-// against these, us: one token, N = 10240, K = 8192 (80 tiles; 143 of 72) 18.6,
-// 16.8; N = 12288, K = 4096 11.9, 11.2; 24 tokens, N = 20480, K = 2560 16.5, 15.6.
-int w8_tile_n(int64_t N, int64_t tiles) {
-    const int64_t rows = round_up((N + tiles - 1) / tiles, 8);
-    return (int)std::clamp<int64_t>(rows, 64, w8n::BN);
-}
-// The kernel and tile whose estimated time is least, in nanoseconds:
-//   pair:   5950 + load(waves x 290 per chunk of 128 bytes of K)
-//   narrow: 2650 + load(waves x chunks of a CTA x t) + (split: 1050 + 96 per token that a CTA finishes)
-// with t = 150, 150, 224, 316 for tiles of 16, 32, 64, 128 tokens and load(x) =
-// the larger of x and the weight's time from HBM (5.7 TB/s) plus a quarter of
-// the smaller.  The constants are fitted to 500 timings at 74 shapes (1 to 2200
-// tokens, N 1024 to 28672, K 1024 to 13824, weights from HBM): the choice is
-// on average 0.1 % slower than the best candidate, at most 9 %.  Examples of
-// both sides: 256 tokens, N = K = 4096: 64-token tiles 9.7 us, pairs 15.7;
-// 1000 tokens: 128-token tiles 24.6, pairs 16.9; one token, N = K = 4096:
-// split in four 6.5, not split 7.8.
-W8Plan w8_plan(int64_t M, int64_t N, int64_t K) {
-    const int64_t chunks = (K + w8n::BK - 1) / w8n::BK;
-    const int64_t weights_ns = N * K / 5700;
-    const auto load = [&](int64_t x) { return std::max(x, weights_ns) + std::min(x, weights_ns) / 4; };
-    const int sms = num_sms();
-    const int mode = g_gemm_tiles_mode.load();
-    W8Plan best = {true, 0, 0, 0, 0};
-    int64_t best_ns = INT64_MAX;
-    if (mode != 1) {
-        const int64_t tiles = ((M + w8p::BM - 1) / w8p::BM) * ((N + w8p::BN - 1) / w8p::BN);
-        const int64_t waves = (tiles + sms / 2 - 1) / (sms / 2);
-        best_ns = 5950 + load(waves * chunks * 290);
-    }
-    if (mode == 2) return best;
-    constexpr int kNt[4] = {16, 32, 64, 128}, kChunkNs[4] = {150, 150, 224, 316};
-    // CTAs of a split that are resident at once: clusters of 4 and 8 leave SMs
-    // of a GPC unused (33 and 15 of them fit 148 SMs).  16 tokens, N = 2560, K =
-    // 13824: 20 tiles split in four 11.2 us, in eight (160 CTAs) 14.8.
-    const int slots[4] = {sms, sms / 2 * 2, sms * 132 / 148, sms * 120 / 148};
-    for (int i = 0; i < 4; ++i) {
-        const int nt = kNt[i];
-        const int64_t mt = (M + nt - 1) / nt, ntl = (N + w8n::BN - 1) / w8n::BN;
-        if (mt > 65535 || ntl > 65535) continue;   // the grid's limits
-        for (int l = 0; l < 4 && (1 << l) <= chunks; ++l) {
-            const int64_t ctas = (mt * ntl) << l, waves = (ctas + slots[l] - 1) / slots[l];
-            if (l > 0 && waves > 1) break;   // a second wave of clusters costs more than a split saves
-            const int64_t of_cta = (chunks + (1 << l) - 1) >> l;
-            int64_t ns = 2650 + load(waves * of_cta * kChunkNs[i]);
-            if (l > 0) ns += 1050 + 96 * ((std::min<int64_t>(M, nt) + (1 << l) - 1) >> l);
-            if (ns < best_ns) {
-                best_ns = ns;
-                const int64_t tiles = std::min<int64_t>(waves * slots[l] / (mt << l), 65535);
-                best = {false, nt, 1 << l, w8_ring(nt, 1 << l, chunks), w8_tile_n(N, tiles)};
+// What the planner needs to know of the current device, asked of the runtime
+// once per device: how many clusters of the narrow kernel's CTAs (one on an SM)
+// are resident at once.
+W8Chip w8_chip() {
+    static std::atomic<int> per_dev[kMaxDevices][4];
+    const int dev = current_device();
+    W8Chip chip;
+    chip.clusters[0] = num_sms();
+    for (int l = 1; l < 4; ++l) {
+        int n = per_dev[dev][l].load();
+        if (n == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << l;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(1u << l, (unsigned)num_sms(), 1);
+            cfg.blockDim = dim3(w8n::kThreads, 1, 1);
+            cfg.dynamicSmemBytes = kW8SmemBudget;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, gemm_w8a8_narrow_kernel<16, kBf16>, &cfg) != cudaSuccess || n <= 0) {
+                cudaGetLastError();
+                n = num_sms() >> l;
             }
+            per_dev[dev][l].store(n);
         }
+        chip.clusters[l] = n;
     }
-    return best;
+    return chip;
 }
 
 template <int NT>
@@ -998,7 +956,7 @@ svdq_status gemm_w8a8_narrow(const W8Plan& p, const CUtensorMap& tm_x, const CUt
 svdq_status gemm_w8a8(const void* x_codes, const float* x_scales, int64_t M, const void* w_codes,
                       const float* w_scales, int64_t N, int64_t K, const void* bias, svdq_dtype out, void* y,
                       cudaStream_t st) {
-    const W8Plan p = w8_plan(M, N, K);
+    const W8Plan p = w8_plan(M, N, K, w8_chip(), g_gemm_tiles_mode.load());
     GemmW8Args a = {};
     a.x_scales = x_scales;
     a.w_scales = w_scales;

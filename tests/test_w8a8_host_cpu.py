@@ -72,6 +72,57 @@ def test_drain_waits_for_the_copies_in_flight_and_no_others(run):
     assert int(out[4]) == rows - 14510000
 
 
+PLAN = """
+// Plans of random shapes (sizes spread over their logarithm) on several chips.
+int main() {
+    const W8Chip chips[] = {{{148, 74, 33, 15}}, {{148, 74, 30, 12}}, {{132, 66, 28, 12}}, {{160, 80, 40, 20}}};
+    unsigned long long seed = 1;
+    const auto uniform = [&] { return (double)((seed = seed * 6364136223846793005ull + 1442695040888963407ull) >> 11) / 9007199254740992.0; };
+    const auto spread = [&](double hi, int64_t step) {
+        int64_t v = 1;
+        for (double x = uniform(); x > 0.0 && (double)v < hi; x -= 0.02) v = v + v / 2 + 1;
+        v = v - (int64_t)(uniform() * (double)(v / 3));
+        return std::max(step, std::min((int64_t)hi, v / step * step));
+    };
+    long plans = 0, narrow = 0, split = 0, bad = 0;
+    for (int i = 0; i < 300000; ++i) {
+        const int64_t M = spread(2147483647.0, 1), N = spread(2147483640.0, 8), K = spread(131056.0, 16);
+        const int64_t chunks = (K + 127) / 128;
+        for (const W8Chip& chip : chips)
+            for (int mode = 0; mode < 3; ++mode) {
+                const W8Plan p = w8_plan(M, N, K, chip, mode);
+                ++plans;
+                if (mode == 2 && !p.pair) ++bad;
+                if (mode == 1 && p.pair && (M + 127) / 128 <= 65535 && (N + 127) / 128 <= 65535) ++bad;
+                if (p.pair) continue;
+                ++narrow;
+                const int64_t mt = (M + p.nt - 1) / p.nt, nt = (N + p.tile_n - 1) / p.tile_n;
+                int l = 0;
+                while ((1 << l) < p.split) ++l;
+                bad += p.nt != 16 && p.nt != 32 && p.nt != 64 && p.nt != 128;
+                bad += p.tile_n < 64 || p.tile_n > 128 || p.tile_n % 8 != 0;
+                bad += mt > 65535 || nt > 65535;
+                bad += (1 << l) != p.split || p.split > 8 || p.split > chunks;
+                // every stage of a CTA's share in one ring place, or places shared evenly by two warps
+                const int64_t most = ((chunks + p.split - 1) / p.split + w8n::per(p.nt) - 1) / w8n::per(p.nt);
+                bad += p.stages < 1 || p.stages > w8n::kMaxStages || (p.stages == 1 ? most != 1 : p.stages % 2 != 0);
+                bad += w8n::fixed_bytes(p.nt, p.split) + p.stages * w8n::stage_bytes(p.nt) > kW8SmemBudget;
+                // no cluster waits for another to end
+                if (p.split > 1) ++split, bad += mt * nt > chip.clusters[l];
+            }
+    }
+    std::printf("%ld plans, %ld narrow, %ld split, %ld bad\\n", plans, narrow, split, bad);
+}
+"""
+
+
+def test_plans_fit_the_chip(run):
+    """Grid limits, ring depths, shared memory, and split tiles that are all resident at once, on chips whose clusters
+    fit in other numbers."""
+    out = run(PLAN).split()
+    assert out[6] == "0" and int(out[2]) > 100000 and int(out[4]) > 10000, out
+
+
 def test_every_wait_site_has_a_number_of_its_own():
     """The device status word names a wait by one byte: two kernels with the same number could not be told apart."""
     sites = {}
