@@ -24,15 +24,24 @@
 // kernels below the blocks are persistent and keep the gains of their columns
 // in registers:
 //   * rows held in registers, the next row's loads issued before the
-//     reduction of the current one (narrow rows, few rows);
-//   * rows streamed through a ring in shared memory (wide rows);
-//   * two passes over the row (rows that neither holds).
+//     reduction of the current one (rows below 16 KB, x and the residual
+//     together, and fp32 norms of up to 4096 columns);
+//   * rows streamed through a ring in shared memory (wider ones);
+//   * two passes over the row (above 16384 columns, or where shared memory does
+//     not hold two rows).
 // One barrier per row in each.  Measured on a B200, data from HBM: norm, bf16,
 // M = 16384, K = 8192 160 us (939 MB: 5.9 TB/s, 0.90 of a measured copy;
 // 891 MB of DRAM traffic in ncu, none of it read twice), M = 4608, K = 4096
 // 24.4 us (0.83), M = 4608, K = 2048 13.8 us (0.73); norm, fp32, M = 16384, K =
 // 4096 148 us (0.90); quantise, bf16, M = 4608, K = 4096 12.6 us (0.69), M =
-// 16384, K = 8192 74 us (0.82); one token, K = 8192 2.6 us, all latency.
+// 16384, K = 8192 74 us (0.82); quantise, fp32, M = 4608, K = 4096 18.4 us
+// (0.78), M = 16384, K = 8192 117 us (0.87); one token, K = 8192 2.6 to 3.2 us,
+// all latency.  With `normed` beside the codes, bf16: M = 16384, K = 8192 214 us
+// (0.86), M = 4608, K = 4096 31.1 us (0.83); `normed` alone 193 (0.85) and 28.3
+// (0.82).  Where there is little to move per value, instruction issue bounds:
+// the norm without a residual, bf16, M = 4608, K = 4096 21.2 us (0.41; ncu: 65 %
+// of the issue slots, a fifth of DRAM), M = 16384, K = 8192 112 us (0.55); the
+// quantiser's 12.6 us above have 53 % of the slots and a third of DRAM.
 #pragma once
 #include "sm100_ptx.cuh"
 #include "w8a8_plan.h"

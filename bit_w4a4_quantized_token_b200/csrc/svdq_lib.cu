@@ -868,7 +868,10 @@ svdq_status quantize_rows_ring(const QuantRowsArgs& a, int blocks, cudaStream_t 
 //   * the ring where a row's bytes (x and residual) reach 16 KB and two rows
 //     fit: norm, M = 4608: K = 4096 24.2 (held 25.7), K = 2048 14.1 (13.9);
 //     norm, M = 16384, K = 8192 160 (held 223); quantise, M = 4608, K = 12288
-//     35.0 (42.6), K = 4096 13.2 (12.6).  Two blocks per SM (four of half
+//     35.0 (42.6), K = 4096 13.2 (12.6).  The count of rows is not asked for:
+//     norm, K = 8176, M = 1 3.2 (3.4), M = 600 9.4 (12.0), M = 2048 21.7 (32.8);
+//     K = 4096, M = 1 2.9 (2.6), M = 600 5.8 (5.8), M = 2048 13.7 (12.1); the
+//     quantiser at K = 8176 the same in both.  Two blocks per SM (four of half
 //     the threads up to 4096 columns) when they can each hold two rows, but
 //     one, with all the memory, for rows of 32 KB in large numbers (M = 16384,
 //     K = 8192: 160 against 170; M = 600: 11.0 against 9.4).

@@ -92,11 +92,17 @@ inline int w8_tile_n(int64_t N, int64_t tiles) {
 // with t = 150, 150, 224, 316 for tiles of 16, 32, 64, 128 tokens and load(x) =
 // the larger of x and the weight's time from HBM (5.7 TB/s) plus a quarter of
 // the smaller.  The constants are fitted to 500 timings at 74 shapes (1 to 2200
-// tokens, N 1024 to 28672, K 1024 to 13824, weights from HBM): the choice is
-// on average 0.1 % slower than the best candidate, at most 9 %.  Examples of
-// both sides: 256 tokens, N = K = 4096: 64-token tiles 9.7 us, pairs 15.7;
-// 1000 tokens: 128-token tiles 24.6, pairs 16.9; one token, N = K = 4096:
-// split in four 6.5, not split 7.8.  mode: 0 both kernels, 1 the narrow one
+// tokens, N 1024 to 28672, K 1024 to 13824, weights from HBM), before narrower
+// tiles and the limit on splits.  As it is now, every candidate timed at 170
+// shapes (1 to 16384 tokens, N 8 to 28672, K 256 to 13824): the choice is the
+// best one at 135, within 10 % of it at 154, 3.6 % slower on average.  The
+// others are mostly of K <= 1040, where what the estimate leaves out is most of
+// the time: the start and end of a narrow tile in each wave (1000 tokens, N =
+// 2560, K = 1040: 128-token tiles 14.4 us, pairs 10.1) and the bytes of x and y
+// (16384 tokens, N = K = 512: 19.3 and 12.0, the worst).  Examples of both
+// sides: 256 tokens, N = K = 4096: 64-token tiles 9.7 us, pairs 15.7; 1000
+// tokens: 128-token tiles 24.6, pairs 16.9; one token, N = K = 4096: split in
+// four 6.5, not split 7.8.  mode: 0 both kernels, 1 the narrow one
 // (where its grid holds the shape), 2 the pair kernel.
 inline W8Plan w8_plan(int64_t M, int64_t N, int64_t K, const W8Chip& chip, int mode) {
     const int64_t chunks = (K + w8n::BK - 1) / w8n::BK;

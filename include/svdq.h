@@ -475,7 +475,9 @@ svdq_status svdq_device_status(int clear, int* site);
  *  svdq_debug_force_gemm_tiles: choose the nvfp4 GEMM kernel: 0 = automatic
  *    (M <= 128: 128 x 256 tiles on single CTAs; M > 128: CTA-pair tiles),
  *    1 = always single CTAs, 2 = always CTA pairs; the same for the W8A8
- *    GEMM (automatic: by its tile counts).  Both kernels compute the
+ *    GEMM (automatic: the kernel and tile of the least estimated time; 1 =
+ *    its tiles of single CTAs, of which up to eight in a cluster may share K,
+ *    except where their grid cannot hold the shape).  Both kernels compute the
  *    same y; this exists so that tests can run each on the same inputs.  Any
  *    other value is SVDQ_ERR_INVALID_ARG. */
 svdq_status svdq_debug_set_wait_limit_ns(uint64_t ns);
